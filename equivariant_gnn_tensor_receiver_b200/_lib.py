@@ -60,6 +60,27 @@ _EXPORTS = {
     "tpconv_forward_static": (ctypes.c_int, [_P, _I64, _I64] + [_P] * 6 + [_P]),
     "tpconv_backward": (ctypes.c_int, [_P, _I64, _I64] + [_P] * 14 + [_P, ctypes.c_size_t, _P]),
     "tpconv_double_backward": (ctypes.c_int, [_P, _I64, _I64] + [_P] * 16 + [_P, ctypes.c_size_t, _P]),
+    "tpconv_group_workspace_size": (ctypes.c_int, [_I64, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "tpconv_group_nodes": (ctypes.c_int, [_I64, ctypes.c_int] + [_P] * 3 + [_P, ctypes.c_size_t, _P]),
+    "tpconv_linear_create": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.c_char_p, ctypes.c_char_p, ctypes.c_int,
+                                            ctypes.c_int]),
+    "tpconv_linear_destroy": (ctypes.c_int, [_P]),
+    "tpconv_linear_info": (ctypes.c_int, [_P] + [ctypes.POINTER(ctypes.c_int)] * 4
+                           + [ctypes.POINTER(ctypes.c_size_t)]),
+    "tpconv_linear_path": (ctypes.c_int, [_P, ctypes.c_int] + [ctypes.POINTER(ctypes.c_int)] * 5
+                           + [ctypes.POINTER(ctypes.c_size_t)]),
+    "tpconv_linear_workspace_size": (ctypes.c_int, [_P, ctypes.c_int, _I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "tpconv_linear_forward": (ctypes.c_int, [_P, _I64] + [_P] * 5 + [_P, ctypes.c_size_t, _P]),
+    "tpconv_linear_backward": (ctypes.c_int, [_P, _I64] + [_P] * 7 + [_P, ctypes.c_size_t, _P]),
+    "tpconv_linear_double_backward": (ctypes.c_int, [_P, _I64] + [_P] * 10 + [_P, ctypes.c_size_t, _P]),
+    "tpconv_linear_device_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_int)]),
+    "tpconv_norm_create": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.c_char_p, ctypes.c_double]),
+    "tpconv_norm_destroy": (ctypes.c_int, [_P]),
+    "tpconv_norm_info": (ctypes.c_int, [_P] + [ctypes.POINTER(ctypes.c_int)] * 4),
+    "tpconv_norm_workspace_size": (ctypes.c_int, [_P, ctypes.c_int, _I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "tpconv_norm_forward": (ctypes.c_int, [_P, _I64] + [_P] * 4 + [_P]),
+    "tpconv_norm_backward": (ctypes.c_int, [_P, _I64] + [_P] * 6 + [_P, ctypes.c_size_t, _P]),
+    "tpconv_norm_double_backward": (ctypes.c_int, [_P, _I64] + [_P] * 9 + [_P, ctypes.c_size_t, _P]),
     "tpconv_get_device_status": (ctypes.c_int, [_P, _P, ctypes.POINTER(ctypes.c_int)]),
     "tpconv_set_wait_limit": (ctypes.c_int, [ctypes.c_uint64]),
     "tpconv_profile_enable": (ctypes.c_int, [ctypes.c_int]),
@@ -68,7 +89,7 @@ _EXPORTS = {
                                            ctypes.POINTER(ctypes.c_int64)]),
 }
 PHASES = ["transpose", "fwd_edge", "fwd_node", "bwd_node_g", "bwd_edge_r", "bwd_edge_s", "bwd_node_x",
-          "dbl_edge_a", "dbl_node_a", "dbl_edge_r", "dbl_edge_s", "dbl_node_x", "other"]
+          "dbl_edge_a", "dbl_node_a", "dbl_edge_r", "dbl_edge_s", "dbl_node_x", "other", "group", "norm", "linear"]
 
 
 def exported_names():
@@ -241,6 +262,132 @@ def tpconv_double_backward(plan, N, E, rowptr, col, perm, s_rowptr, s_recv, edge
                                         _ptr(gg_vec, f32), _ptr(gg_theta, f32), _ptr(d_g, f32),
                                         _ptr(d_x, f32), _ptr(d_vec, f32), _ptr(d_theta, f32), w, wb,
                                         _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# node operators: grouping by type, typed linear map, layer norm
+# --------------------------------------------------------------------------
+MAX_TYPES = 256  # TPCONV_MAX_TYPES
+
+
+class LinearPlan:
+    """Owner of a ``tpconv_linear*``: the typed linear map irreps_in -> irreps_out with one weight
+    per node type.  ``paths`` lists the weight's blocks ([c_in][c_out] at ``weight_offset``)."""
+
+    def __init__(self, irreps_in, irreps_out, n_types=1, gemm="fp32"):
+        h = _P()
+        _check("tpconv_linear_create",
+               lib().tpconv_linear_create(ctypes.byref(h), irreps_in.encode(), irreps_out.encode(), int(n_types),
+                                          GEMM[gemm]))
+        self.handle = h
+        self.irreps_in, self.irreps_out, self.n_types, self.gemm = irreps_in, irreps_out, int(n_types), gemm
+        a = [ctypes.c_int() for _ in range(4)]
+        w = ctypes.c_size_t()
+        _check("tpconv_linear_info", lib().tpconv_linear_info(h, *[ctypes.byref(v) for v in a], ctypes.byref(w)))
+        self.n_paths, self.dim_in, self.dim_out, _ = (v.value for v in a)
+        self.weight_numel = w.value
+        self.paths = []
+        for i in range(self.n_paths):
+            v = [ctypes.c_int() for _ in range(5)]
+            _check("tpconv_linear_path", lib().tpconv_linear_path(h, i, *[ctypes.byref(x) for x in v],
+                                                                  ctypes.byref(w)))
+            l, ci, co, ib, ob = (x.value for x in v)
+            self.paths.append(dict(l=l, c_in=ci, c_out=co, in_block=ib, out_block=ob, weight_offset=w.value))
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and _lib is not None:
+            _lib.tpconv_linear_destroy(h)
+            self.handle = None
+
+
+class NormPlan:
+    """Owner of a ``tpconv_norm*``: the layer norm of irreps features."""
+
+    def __init__(self, irreps, eps=1e-5):
+        h = _P()
+        _check("tpconv_norm_create", lib().tpconv_norm_create(ctypes.byref(h), irreps.encode(), float(eps)))
+        self.handle = h
+        self.irreps, self.eps = irreps, float(eps)
+        a = [ctypes.c_int() for _ in range(4)]
+        _check("tpconv_norm_info", lib().tpconv_norm_info(h, *[ctypes.byref(v) for v in a]))
+        self.n_blocks, self.dim, self.weight_numel, self.bias_numel = (v.value for v in a)
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and _lib is not None:
+            _lib.tpconv_norm_destroy(h)
+            self.handle = None
+
+
+def tpconv_group_workspace_size(N, n_types) -> int:
+    b = ctypes.c_size_t()
+    _check("tpconv_group_workspace_size", lib().tpconv_group_workspace_size(N, n_types, ctypes.byref(b)))
+    return b.value
+
+
+def tpconv_linear_workspace_size(plan: LinearPlan, op: int, N: int) -> int:
+    b = ctypes.c_size_t()
+    _check("tpconv_linear_workspace_size", lib().tpconv_linear_workspace_size(plan.handle, op, N, ctypes.byref(b)))
+    return b.value
+
+
+def tpconv_norm_workspace_size(plan: NormPlan, op: int, N: int) -> int:
+    b = ctypes.c_size_t()
+    _check("tpconv_norm_workspace_size", lib().tpconv_norm_workspace_size(plan.handle, op, N, ctypes.byref(b)))
+    return b.value
+
+
+def tpconv_group_nodes(N, n_types, type, perm, offsets, workspace, stream=None):
+    import torch
+    i32 = torch.int32
+    w, wb = _ws(workspace)
+    _check("tpconv_group_nodes", lib().tpconv_group_nodes(N, n_types, _ptr(type, i32), _ptr(perm, i32),
+                                                          _ptr(offsets, i32), w, wb, _stream(stream)))
+
+
+def _call(name, plan, N, ints, floats, workspace, stream):
+    import torch
+    args = [_ptr(t, torch.int32) for t in ints] + [_ptr(t, torch.float32) for t in floats]
+    if workspace is not False:
+        args += list(_ws(workspace))
+    _check(name, getattr(lib(), name)(plan.handle, N, *args, _stream(stream)))
+
+
+def tpconv_linear_forward(plan, N, perm, offsets, x, weight, out, workspace, stream=None):
+    _call("tpconv_linear_forward", plan, N, (perm, offsets), (x, weight, out), workspace, stream)
+
+
+def tpconv_linear_backward(plan, N, perm, offsets, x, weight, g, dx, dweight, workspace, stream=None):
+    _call("tpconv_linear_backward", plan, N, (perm, offsets), (x, weight, g, dx, dweight), workspace, stream)
+
+
+def tpconv_linear_double_backward(plan, N, perm, offsets, x, weight, g, gg_x, gg_weight, d_g, d_x, d_weight,
+                                  workspace, stream=None):
+    _call("tpconv_linear_double_backward", plan, N, (perm, offsets),
+          (x, weight, g, gg_x, gg_weight, d_g, d_x, d_weight), workspace, stream)
+
+
+def tpconv_linear_device_status(plan, stream=None) -> int:
+    """As ``tpconv_get_device_status``, for the tensor-core kernels of the typed linear map."""
+    st = ctypes.c_int()
+    _check("tpconv_linear_device_status",
+           lib().tpconv_linear_device_status(plan.handle, _stream(stream), ctypes.byref(st)))
+    return st.value
+
+
+def tpconv_norm_forward(plan, N, x, weight, bias, y, stream=None):
+    _call("tpconv_norm_forward", plan, N, (), (x, weight, bias, y), False, stream)
+
+
+def tpconv_norm_backward(plan, N, x, weight, g, dx, dweight, dbias, workspace, stream=None):
+    _call("tpconv_norm_backward", plan, N, (), (x, weight, g, dx, dweight, dbias), workspace, stream)
+
+
+def tpconv_norm_double_backward(plan, N, x, weight, g, gg_x, gg_weight, gg_bias, d_g, d_x, d_weight, workspace,
+                                stream=None):
+    _call("tpconv_norm_double_backward", plan, N, (), (x, weight, g, gg_x, gg_weight, gg_bias, d_g, d_x, d_weight),
+          workspace, stream)
 
 
 TPCONV_ERR_TIMEOUT = 7

@@ -15,6 +15,7 @@
 #include <string>
 #include <vector>
 
+#include "irreps.h"
 #include "plan.h"
 #include "wn_layout.h"
 #include "workspace.h"
@@ -173,11 +174,7 @@ const float* tpc::cg_table_f32() {
 // ---------------------------------------------------------------------------
 // irreps parsing
 // ---------------------------------------------------------------------------
-namespace {
-struct Blk {
-  int mul, l, p;
-};
-
+namespace tpc {
 int parse_irreps(const char* s, std::vector<Blk>& out) {
   out.clear();
   if (!s) return TPCONV_ERR_INVALID_ARG;
@@ -210,7 +207,7 @@ int parse_irreps(const char* s, std::vector<Blk>& out) {
   if (out.size() > size_t(kMaxBlocks)) return TPCONV_ERR_UNSUPPORTED;
   return TPCONV_OK;
 }
-}  // namespace
+}  // namespace tpc
 
 // ---------------------------------------------------------------------------
 // public host API

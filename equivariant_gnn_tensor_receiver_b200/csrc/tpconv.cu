@@ -16,6 +16,7 @@
 #include <atomic>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "gemm_simt.cuh"
@@ -25,6 +26,7 @@
 #include "gemm_tc.h"
 #include "graph.cuh"
 #include "launchers.h"
+#include "node_ops.h"
 #include "plan.h"
 #include "wn_layout.h"
 #include "workspace.h"
@@ -527,6 +529,15 @@ int finish_call(const tpconv_plan* plan, cudaStream_t s, cudaError_t e) {
 }
 
 }  // namespace
+
+namespace tpc {
+NodePhase::NodePhase(int phase, cudaStream_t st) : phase_(phase), scope_(nullptr) {
+  if (prof().on) scope_ = new (std::nothrow) PhaseScope(phase, st);
+}
+NodePhase::~NodePhase() { delete static_cast<PhaseScope*>(scope_); }
+void NodePhase::note(int64_t launches) { ::note(phase_, launches); }
+uint64_t device_wait_limit() { return wait_ns(); }
+}  // namespace tpc
 
 extern "C" {
 

@@ -250,6 +250,107 @@ int tpconv_double_backward(const tpconv_plan* plan, int64_t N, int64_t E, const 
                            float* d_vec, float* d_theta, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Node operators around the convolution: nodes grouped by type, the typed
+ * linear map and the layer norm of irreps features.  Features and conventions
+ * are those at the top of this file (fp32, contiguous, [mul][2l+1] blocks,
+ * caller-owned memory, asynchronous on the stream, outputs overwritten).
+ * They need no one-time device set-up, so their first call may be a captured
+ * one.  No output may overlap an input or another output
+ * (TPCONV_ERR_INVALID_ARG).  The pages define none of them: they are additions
+ * of this library (what a layer of such a network holds next to the
+ * convolution), with formulas of their own below.
+ * ------------------------------------------------------------------------- */
+
+/* ---- nodes grouped by type ------------------------------------------------
+ * type[N] (device) holds a type in [0, n_types); any other value puts the node
+ * in no group (padding rows of a batch).
+ *   perm[N]            out: node ids by type, ascending inside a type; the
+ *                           nodes of no group behind all types, ascending.
+ *   offsets[n_types+1] out: type t owns perm[offsets[t] : offsets[t + 1]].
+ * n_types is 1..TPCONV_MAX_TYPES, N below 2^31. */
+#define TPCONV_MAX_TYPES 256
+int tpconv_group_workspace_size(int64_t N, int n_types, size_t* bytes);
+int tpconv_group_nodes(int64_t N, int n_types, const int32_t* type, int32_t* perm, int32_t* offsets,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- typed linear map -----------------------------------------------------
+ *   out[n, i3, w, m] = sum_{p -> i3} sum_u W[type(n)][p][u][w] x[n, i1(p), u, m]
+ * with one path p per pair (output block i3, input block i1) of equal degree
+ * and parity, in that order.  W is [n_types][weight_numel], a path's block
+ * [C_in][C_out] at its offset; no normalisation is applied.  An output block
+ * without a path is zero, and so are the rows of nodes in no group (in out, dx,
+ * d_g and d_x); they add nothing to dweight / d_weight.
+ * perm / offsets come from tpconv_group_nodes for the same N and n_types.
+ * (Entries outside [0, N] are never followed; the rows they stand for are
+ * then undefined.)
+ *   gemm: TPCONV_GEMM_FP32 / _TF32 / _SIMT as in tpconv_options.  The tensor-
+ *   core modes need blocks whose multiplicities are multiples of 4, rows a
+ *   multiple of 16 bytes and 16-byte aligned tensors; other calls run on the
+ *   FP32 pipes, whatever the mode. */
+typedef struct tpconv_linear tpconv_linear;
+int tpconv_linear_create(tpconv_linear** out, const char* irreps_in, const char* irreps_out,
+                         int n_types, int gemm);
+int tpconv_linear_destroy(tpconv_linear* plan);
+/* Sizes (host); any pointer may be NULL.  weight_numel is that of one type. */
+int tpconv_linear_info(const tpconv_linear* plan, int* n_paths, int* dim_in, int* dim_out,
+                       int* n_types, size_t* weight_numel);
+/* Path i (host): degree, multiplicities, blocks and the offset of its weight. */
+int tpconv_linear_path(const tpconv_linear* plan, int i, int* l, int* c_in, int* c_out,
+                       int* in_block, int* out_block, size_t* weight_offset);
+/* Bytes of workspace of one call of `op` (TPCONV_OP_FORWARD, _BACKWARD,
+ * _DOUBLE_BACKWARD) for N nodes. */
+int tpconv_linear_workspace_size(const tpconv_linear* plan, int op, int64_t N, size_t* bytes);
+int tpconv_linear_forward(const tpconv_linear* plan, int64_t N, const int32_t* perm,
+                          const int32_t* offsets, const float* x, const float* weight, float* out,
+                          void* workspace, size_t workspace_bytes, void* stream);
+/* dx[N][dim_in], dweight[n_types][weight_numel] for the cotangent g[N][dim_out];
+ * either may be NULL.  The weight gradient is summed in a fixed order. */
+int tpconv_linear_backward(const tpconv_linear* plan, int64_t N, const int32_t* perm,
+                           const int32_t* offsets, const float* x, const float* weight,
+                           const float* g, float* dx, float* dweight, void* workspace,
+                           size_t workspace_bytes, void* stream);
+/* Gradients of <gg_x, dx> + <gg_weight, dweight> by g, x and weight.  A
+ * cotangent gg_* may be NULL (= zero), an output NULL (= not computed). */
+int tpconv_linear_double_backward(const tpconv_linear* plan, int64_t N, const int32_t* perm,
+                                  const int32_t* offsets, const float* x, const float* weight,
+                                  const float* g, const float* gg_x, const float* gg_weight,
+                                  float* d_g, float* d_x, float* d_weight, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+/* As tpconv_get_device_status, for the tensor-core kernels of the linear map. */
+int tpconv_linear_device_status(const tpconv_linear* plan, void* stream, int* status);
+
+/* ---- layer norm of irreps features -----------------------------------------
+ * Per node and block b of C channels, S = C (2l+1) entries:
+ *   xc = x - mean_u x (l = 0), xc = x (l > 0),  r = (sum xc^2 / S + eps)^(-1/2),
+ *   y[u, m] = weight[b, u] r xc[u, m]  (+ bias[b, u] for blocks 0e).
+ * weight holds the C entries of every block in order, bias those of the 0e
+ * blocks; NULL stands for ones and for zeros.  On scalars alone this is the
+ * plain layer norm.  A block has at most TPCONV_NORM_MAX_DIM floats in a row,
+ * and so has the row. */
+#define TPCONV_NORM_MAX_DIM 10240
+typedef struct tpconv_norm tpconv_norm;
+/* eps must be positive and finite. */
+int tpconv_norm_create(tpconv_norm** out, const char* irreps, double eps);
+int tpconv_norm_destroy(tpconv_norm* plan);
+int tpconv_norm_info(const tpconv_norm* plan, int* n_blocks, int* dim, int* weight_numel, int* bias_numel);
+int tpconv_norm_workspace_size(const tpconv_norm* plan, int op, int64_t N, size_t* bytes);
+int tpconv_norm_forward(const tpconv_norm* plan, int64_t N, const float* x, const float* weight,
+                        const float* bias, float* y, void* stream);
+/* dx[N][dim], dweight, dbias for the cotangent g of y; each may be NULL.  The
+ * statistics are computed again from x.  dweight and dbias are summed in a
+ * fixed order. */
+int tpconv_norm_backward(const tpconv_norm* plan, int64_t N, const float* x, const float* weight,
+                         const float* g, float* dx, float* dweight, float* dbias, void* workspace,
+                         size_t workspace_bytes, void* stream);
+/* Gradients of <gg_x, dx> + <gg_weight, dweight> + <gg_bias, dbias> by g, x and
+ * weight.  A cotangent gg_* may be NULL (= zero), an output NULL. */
+int tpconv_norm_double_backward(const tpconv_norm* plan, int64_t N, const float* x,
+                                const float* weight, const float* g, const float* gg_x,
+                                const float* gg_weight, const float* gg_bias, float* d_g,
+                                float* d_x, float* d_weight, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /*
  * Device-side wait status (host; synchronises the stream).  The tensor-core
  * kernels (Theta contractions and Theta gradient) wait only on their own
@@ -294,7 +395,10 @@ int tpconv_set_wait_limit(uint64_t ns);
 #define TPCONV_PHASE_DBL_EDGE_S 10 /* double backward sender stream -> B0, B1  */
 #define TPCONV_PHASE_DBL_NODE_X 11 /* d_x, d_theta                             */
 #define TPCONV_PHASE_OTHER 12      /* memsets, packing, G for double backward  */
-#define TPCONV_N_PHASES 13
+#define TPCONV_PHASE_GROUP 13      /* nodes by type                            */
+#define TPCONV_PHASE_NORM 14       /* layer norm, its gradients                */
+#define TPCONV_PHASE_LINEAR 15     /* typed linear map, its gradients          */
+#define TPCONV_N_PHASES 16
 
 int tpconv_profile_enable(int on);  /* 1: record events from now on; 0: stop    */
 int tpconv_profile_reset(void);     /* drop recorded events and launch counts   */

@@ -20,6 +20,8 @@ What it computes (all fp64, numpy):
               backward are the explicit adjoints of that schedule.  Two
               operator families: "full" (Theta[p] is R x C_in x C_out) and
               "channelwise" (Theta[p] is R x C, W_e[p] diagonal).
+* ``node``    the node operators (grouping by type, typed linear map, layer norm of
+              irreps features) and their first- and second-order gradients.
 
 Sources: "Sobek: streaming edge-conditioned equivariant tensor-product
 convolution" (arXiv 2607.18074), abstract -- the operator (radial projection,
@@ -35,4 +37,4 @@ finite differences, brute force, special cases).  Parity unpinned: absolute
 output values for the pages' own workloads, which the pages do not print.
 """
 
-from . import irreps, radial, so3, conv  # noqa: F401
+from . import irreps, radial, so3, conv, node  # noqa: F401
