@@ -19,7 +19,8 @@
 #include <vector>
 
 #include "irreps.h"
-#include "linear.h"
+#include "linear_grad_tc.h"
+#include "linear_tc.h"
 #include "node_ops.h"
 
 namespace tpc {
@@ -289,6 +290,10 @@ void fill_rows(const tpconv_linear* p, bool transposed, int pairs, LinRows* R) {
 }
 
 cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph, cudaStream_t st) {
+  if (p->gemm != TPCONV_GEMM_SIMT && linear_tc_supported(R)) {
+    ph.note(1);
+    return linear_tc_rows(R, p->gemm == TPCONV_GEMM_FP32, device_wait_limit(), st);
+  }
   int colt = 1, dmax = 1;
   for (int b = 0; b < R.n_out; ++b) {
     colt = std::max(colt, ceil_div(R.o[b].n, kTC));
@@ -309,9 +314,13 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
   G.n_paths = p->n_paths, G.T = p->T, G.N = N, G.wnumel = p->wnumel;
   G.dim_x = p->dim_in, G.dim_g = p->dim_out;
   G.x = x, G.g = g, G.dw = dw, G.perm = perm, G.offsets = offsets;
+  std::copy(p->path, p->path + p->n_paths, G.p);
+  if (p->gemm != TPCONV_GEMM_SIMT && linear_grad_tc_supported(G)) {
+    ph.note(2);
+    return linear_grad_tc(G, p->gemm == TPCONV_GEMM_FP32, part, device_wait_limit(), st);
+  }
   int cu = 1, cw = 1;
   for (int i = 0; i < p->n_paths; ++i) {
-    G.p[i] = p->path[i];
     cu = std::max(cu, ceil_div(G.p[i].ci, kTR));
     cw = std::max(cw, ceil_div(G.p[i].co, kTC));
   }
@@ -329,8 +338,10 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
 }
 
 size_t ws_bytes(const tpconv_linear* p, int op, int64_t N) {
-  if (op == TPCONV_OP_FORWARD) return 0;
-  return (grad_partials(p, N) + 255) & ~size_t(255);
+  if (op == TPCONV_OP_FORWARD || N == 0) return 0;
+  // whichever kernel the call's alignment leads to
+  const size_t tc = p->gemm == TPCONV_GEMM_SIMT ? 0 : linear_grad_tc_bytes(p->path, p->n_paths, p->T, N);
+  return (std::max(grad_partials(p, N), tc) + 255) & ~size_t(255);
 }
 
 bool floats_ok(std::initializer_list<const void*> ps) {
@@ -556,7 +567,11 @@ int tpconv_linear_double_backward(const tpconv_linear* plan, int64_t N, const in
 int tpconv_linear_device_status(const tpconv_linear* plan, void* stream, int* status) {
   if (!plan || !status) return TPCONV_ERR_INVALID_ARG;
   *status = TPCONV_OK;
-  return cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) == cudaSuccess ? TPCONV_OK : TPCONV_ERR_CUDA;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TPCONV_ERR_CUDA;
+  int a = 0, b = 0;
+  if (linear_tc_read_error(&a) != cudaSuccess || linear_grad_tc_read_error(&b) != cudaSuccess) return TPCONV_ERR_CUDA;
+  if (a || b) *status = TPCONV_ERR_TIMEOUT;
+  return TPCONV_OK;
 }
 
 }  // extern "C"

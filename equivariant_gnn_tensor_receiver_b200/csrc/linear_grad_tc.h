@@ -1,0 +1,19 @@
+// Weight gradient of the typed linear map on the tensor cores (linear_grad_tc.cu).
+#pragma once
+
+#include "linear.h"
+
+namespace tpc {
+
+constexpr int kLinGradTcEntries = 64;  // (path, channel tile) pairs of a call
+
+// whether every block and tensor can be copied 16 bytes at a time
+bool linear_grad_tc_supported(const LinGrad& G);
+// bytes of the partial tiles of a call
+size_t linear_grad_tc_bytes(const LinPath* path, int n, int T, int64_t N);
+// dW (and zeros for empty types); split = 3xTF32, else one TF32 pass.  Two launches.
+cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t limit, cudaStream_t st);
+// first code recorded by an expired wait since the last read (0 = none); clears it
+cudaError_t linear_grad_tc_read_error(int* code);
+
+}  // namespace tpc

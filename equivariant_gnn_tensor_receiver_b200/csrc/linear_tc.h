@@ -1,0 +1,18 @@
+// Typed linear map on the tensor cores (linear_tc.cu).
+#pragma once
+
+#include "linear.h"
+
+namespace tpc {
+
+constexpr int kLinTcChunks = 4;    // 64-channel chunks of a resident weight: up to 256 source channels
+constexpr int kLinTcEntries = 64;  // (output block, 64 columns) pairs of a call
+
+// whether every block and tensor of the product can be copied 16 bytes at a time and its weights stay resident
+bool linear_tc_supported(const LinRows& R);
+// the row product; split = 3xTF32, else one TF32 pass
+cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStream_t st);
+// first code recorded by an expired wait since the last read (0 = none); clears it
+cudaError_t linear_tc_read_error(int* code);
+
+}  // namespace tpc

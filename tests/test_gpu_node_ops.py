@@ -445,3 +445,30 @@ def test_modules_as_a_training_program_uses_them(T):
     G = T.NodeGroups(torch.zeros(30, dtype=torch.int32, device="cuda"), 2)
     lin(x, G).sum().backward()  # an expanded cotangent, no weight gradient wanted
     assert lin.weight.grad is None and x.grad is not None
+
+
+def test_expired_waits_are_reported_and_recovered(T):
+    """With a wait limit of 1 ns the tensor-core kernels' bounded waits run out on purpose: the call returns, the
+    status says so once, and the next call is right again."""
+    import torch
+    L = T._lib
+    irr = ("64x0e+64x1o+64x2e",) * 2
+    t, d = linear_inputs(irr, 3000, 4, 2)
+    p = T.LinearPlan(*irr, n_types=4)
+    G = T.NodeGroups(dev(t, torch.int32), 4)
+    x, w, g = dev(d["x"]), dev(d["w"]), dev(d["g"])
+    want = (T.linear_forward(p, G, x, w), T.linear_backward(p, G, x, w, g, want=("dweight",))["dweight"])
+    assert L.tpconv_linear_device_status(p) == L.TPCONV_OK
+    try:
+        L.tpconv_set_wait_limit(1)
+        T.linear_forward(p, G, x, w)
+        a = L.tpconv_linear_device_status(p)
+        T.linear_backward(p, G, x, w, g, want=("dweight",))
+        b = L.tpconv_linear_device_status(p)
+    finally:
+        L.tpconv_set_wait_limit(0)
+    assert (a, b) == (L.TPCONV_ERR_TIMEOUT, L.TPCONV_ERR_TIMEOUT)
+    assert L.tpconv_linear_device_status(p) == L.TPCONV_OK
+    got = (T.linear_forward(p, G, x, w), T.linear_backward(p, G, x, w, g, want=("dweight",))["dweight"])
+    assert L.tpconv_linear_device_status(p) == L.TPCONV_OK
+    assert all(torch.equal(u, v) for u, v in zip(got, want))
