@@ -5,8 +5,8 @@
 //
 // per path, 128 input channels and 64 output channels: a product whose depth is the
 // ragged row count of the type.  A chunk is the rows of 64, 16, 8 or 8 nodes
-// (l = 0..3: 64, 48, 40, 56 rows); bulk copies gather the nodes' pieces of x and g by
-// perm.  The A operand is x transposed: thread u reads its channel of every row (the
+// (l = 0..3: 64, 48, 40, 56 rows); copy threads gather the nodes' pieces of x and g by
+// perm, 16 bytes a thread (4 where a block or tensor is not aligned for it).  The A operand is x transposed: thread u reads its channel of every row (the
 // lanes of a warp are 2l+1 floats apart: no bank conflicts), splits it (3xTF32) and
 // stores hi and lo to TMEM, lane = u, column = row.  The B operand is g: thread w
 // reads its channel and writes hi and lo into the K-major 128-byte-swizzled tile.  One
@@ -22,12 +22,13 @@
 //
 // Bound: HBM (x and g read once), next to shared memory: a row of 64 + 64 channels
 // is 512 B from HBM and about 2.3 KB of shared-memory traffic.
-// Warps 0-3 convert x, 4-7 convert g, 8-11 add finished banks and store, 12 issues
-// copies, 13 MMAs.  Waits are bounded as in the row kernel.
+// Warps 0-3 convert x, 4-7 convert g, 8-11 add finished banks and store, 12-14
+// copy, 15 issues the MMAs.  Waits are bounded as in the row kernel.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "linear_grad_tc.h"
 #include "linear_tc_common.cuh"
@@ -39,25 +40,38 @@ using namespace tc;
 
 __device__ int g_linear_grad_error;  // first code recorded by an expired wait (0 = none)
 
+constexpr int kSMs = 148;                     // CTAs of a call, at most
 constexpr int kMT = 128, kNT = 64;            // input and output channels of a tile
 constexpr int kKMax = 64;                     // rows of a chunk, at most
 constexpr int kRound = 3;                     // chunks accumulated in TMEM before they are added up
 constexpr int kBTile = kNT * kKMax * 4;       // 16 KB: hi or lo of a B chunk
 constexpr int kMaxStages = 6;
 constexpr int kSMemMax = 227 * 1024;
-constexpr int kThreads = 448;
+constexpr int kThreads = 512;
+constexpr int kCopy = 96;                     // copy threads
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemA = 0, kTmemAStage = 2 * kKMax, kTmemD = 256;
 
 // nodes and rows of a chunk
 __host__ __device__ constexpr int chunk_nodes(int d) { return d == 1 ? 64 : (d == 3 ? 16 : 8); }
-__host__ __device__ inline int tiles_u(const LinPath& p) { return (p.ci + kMT - 1) / kMT; }
-__host__ __device__ inline int tiles_w(const LinPath& p) { return (p.co + kNT - 1) / kNT; }
-// cost of a chunk: the bytes it moves, in units of 1 KB
-__host__ __device__ inline int chunk_cost(const LinPath& p, int u0, int w0) {
-  const int cu = p.ci - u0 < kMT ? p.ci - u0 : kMT, cw = p.co - w0 < kNT ? p.co - w0 : kNT;
-  return 1 + (cu + cw) * p.d * chunk_nodes(p.d) / 256;
-}
+
+// (path, 128 input channels, 64 output channels)
+struct Entry {
+  int d, cost;      // 2l+1; cost of a chunk
+  int xoff, goff;   // first columns in x and g
+  int cu, cw;       // channels
+  int co, pad;      // output channels of the path: the pitch of its weight
+  int64_t woff;     // first weight
+};
+struct Params {
+  int n_entries, T, dim_x, dim_g;
+  int64_t N, wnumel;
+  const float *x, *g;
+  float* dw;
+  const int *perm, *offsets;
+  int coef[4];  // cost of a chunk of d = 1, 3, 5, 7, summed over the entries
+  Entry e[kLinGradTcEntries];
+};
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -65,147 +79,111 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int total[4];  // chunks of all types for d = 1, 3, 5, 7
-  int start_t, start_j;
+  int node[2][64];
 };
 
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, uint64_t limit, volatile int* abort, int code) {
   return wait_or_abort(b, parity, limit, abort, &g_linear_grad_error, code);
 }
 
-// chunks of all types per degree: warp i (of the first four) for d = 2i + 1
-__device__ __forceinline__ void count_chunks(const LinGrad& P, int* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp >= 4) return;
-  const int unit = chunk_nodes(2 * warp + 1);
-  int s = 0;
-  for (int t = lane; t < P.T; t += 32) {
-    int b, e;
-    lin_group(P.offsets, P.T, P.N, t, &b, &e);
-    s += (e - b + unit - 1) / unit;
-  }
-  s = __reduce_add_sync(0xffffffffu, s);
-  if (lane == 0) total[warp] = s;
-}
-__device__ __forceinline__ int64_t total_cost(const LinGrad& P, const int* total) {
+__device__ __forceinline__ int64_t total_cost(const Params& P, const int* total) {
   int64_t c = 0;
-  for (int p = 0; p < P.n_paths; ++p)
-    for (int u = 0; u < tiles_u(P.p[p]); ++u)
-      for (int w = 0; w < tiles_w(P.p[p]); ++w)
-        c += int64_t(total[P.p[p].d >> 1]) * chunk_cost(P.p[p], u * kMT, w * kNT);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c += int64_t(total[i]) * P.coef[i];
   return c;
 }
-__device__ __forceinline__ int64_t share_begin(int64_t total, int b, int ctas) { return total * b / ctas; }
 
 // a run of chunks of one type in one entry
 struct Piece {
-  int p, u0, w0, t, first, nodes;
+  int e, t, first, nodes;
   int slot;  // partial tile, or -1: the type's rows are all here
 };
 
+// CTA b owns the chunks whose cost begins in its share.  Every warp walks the same list.
 struct Walk {
-  const LinGrad& P;
-  const Shared& sh;
+  const Entry* E;
+  const int* offs;
+  const int* total;
+  int n_entries, T;
   int64_t lo, hi, base = 0, left = 0;
-  int p = -1, u = 0, w = 0;
-  int t = 0, j = 0, gb = 0, ge = 0, n = 0;
-  bool first_entry = true;
+  int e = -1, unit = 1, t = 0, j = 0, n = 0;
 
-  __device__ Walk(const LinGrad& g, const Shared& s, int64_t total) : P(g), sh(s) {
-    lo = share_begin(total, blockIdx.x, gridDim.x);
-    hi = share_begin(total, blockIdx.x + 1, gridDim.x);
-  }
-  __device__ bool next_entry(int64_t* j0) {
-    for (;;) {
-      if (p < 0) {
-        p = 0;
-      } else {
-        base += int64_t(sh.total[P.p[p].d >> 1]) * chunk_cost(P.p[p], u * kMT, w * kNT);
-        if (++w >= tiles_w(P.p[p])) {
-          w = 0;
-          if (++u >= tiles_u(P.p[p])) u = 0, ++p;
-        }
-      }
-      if (p >= P.n_paths || base >= hi) return false;
-      const int c = chunk_cost(P.p[p], u * kMT, w * kNT);
-      const int64_t all = sh.total[P.p[p].d >> 1];
-      const int64_t a = lo <= base ? 0 : min((lo - base + c - 1) / c, all), b = min((hi - base + c - 1) / c, all);
-      if (a < b) {
-        left = b - a;
-        *j0 = a;
-        return true;
-      }
-    }
-  }
-  __device__ void load_group() {
-    lin_group(P.offsets, P.T, P.N, t, &gb, &ge);
-    const int unit = chunk_nodes(P.p[p].d);
-    n = (ge - gb + unit - 1) / unit;
+  __device__ Walk(const Params& P, const Entry* entries, const int* o, const int* tot)
+      : E(entries), offs(o), total(tot), n_entries(P.n_entries), T(P.T) {
+    const int64_t c = total_cost(P, tot);
+    lo = share_begin(c, blockIdx.x, gridDim.x);
+    hi = share_begin(c, blockIdx.x + 1, gridDim.x);
   }
   __device__ bool next(Piece* q) {
     if (left == 0) {
-      int64_t j0;
-      if (!next_entry(&j0)) return false;
-      if (first_entry) {
-        t = sh.start_t, j = sh.start_j;
-        first_entry = false;
-      } else {
-        t = 0, j = 0;
+      for (;;) {
+        if (e >= 0) base += int64_t(total[E[e].d >> 1]) * E[e].cost;
+        if (++e >= n_entries || base >= hi) {
+          e = n_entries;
+          return false;
+        }
+        const int c = E[e].cost;
+        const int64_t all = total[E[e].d >> 1];
+        const int64_t a = lo <= base ? 0 : min(div_cost(lo - base + c - 1, c), all),
+                      b = min(div_cost(hi - base + c - 1, c), all);
+        if (a < b) {
+          left = b - a;
+          unit = chunk_nodes(E[e].d);
+          seek_unit(offs, T, unit, a, &t, &j);
+          n = t < T ? group_units(offs, t, unit) : 0;
+          break;
+        }
       }
-      load_group();
     }
     while (j >= n) {
-      if (t + 1 >= P.T) return false;
+      if (t + 1 >= T) return false;
       ++t, j = 0;
-      load_group();
+      n = group_units(offs, t, unit);
     }
-    const int unit = chunk_nodes(P.p[p].d), c = int(min(int64_t(n - j), left));
-    q->p = p, q->u0 = u * kMT, q->w0 = w * kNT, q->t = t;
-    q->first = gb + j * unit;
-    q->nodes = min(ge - q->first, c * unit);
+    const int c = int(min(int64_t(n - j), left));
+    q->e = e, q->t = t;
+    q->first = offs[t] + j * unit;
+    q->nodes = min(offs[t + 1] - q->first, c * unit);
     q->slot = (j == 0 && c == n) ? -1 : 2 * int(blockIdx.x) + (j == 0);
     j += c, left -= c;
     return true;
   }
 };
 
-// thread u: its channel of rows k0 .. k0+7 of the chunk (zeros at and behind kv)
-template <int D>
+// thread u: its channel of rows K0 .. K0+7 of the chunk (zeros at and behind kv)
+template <int D, bool WHOLE>
 __device__ __forceinline__ void read8(const float* col, int pitch, int k0, int kv, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int k = k0 + i;
-    v[i] = k < kv ? col[(k / D) * pitch + k % D] : 0.f;
+    v[i] = (WHOLE || k < kv) ? col[(k / D) * pitch + k % D] : 0.f;
   }
 }
-template <int D, bool SPLIT>
-__device__ __forceinline__ void convert_a(const float* raw, int u, int cu, int kv, uint32_t ta) {
+template <int D, bool SPLIT, bool WHOLE>
+__device__ __forceinline__ void convert_a(const float* col, int pitch, int kv, uint32_t ta) {
   constexpr int ROWS = chunk_nodes(D) * D;
-  const float* col = raw + min(u, cu - 1) * D;
-  const int pitch = cu * D;
-#pragma unroll 2
-  for (int k0 = 0; k0 < ROWS; k0 += 8) {
-    if (k0 >= kv) break;
-    float v[8], h[8];
-    read8<D>(col, pitch, k0, kv, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = rn_tf32(v[i]), v[i] = rn_tf32(v[i] - h[i]);
+  for (int k0 = 0; k0 < ROWS; k0 += 8) {
+    if (!WHOLE && k0 >= kv) break;
+    float v[8], h[8];
+    read8<D, WHOLE>(col, pitch, k0, kv, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tf32_split<SPLIT>(v[i], h[i], v[i]);
     tmem_st8(ta + k0, h);
     if (SPLIT) tmem_st8(ta + kKMax + k0, v);
   }
 }
 // thread (w, half): every second group of 8 rows of its channel, into the swizzled tile
-template <int D, bool SPLIT>
-__device__ __forceinline__ void convert_b(const float* raw, int w, int half, int cw, int kv, unsigned char* hi) {
+template <int D, bool SPLIT, bool WHOLE, int HALF>
+__device__ __forceinline__ void convert_b(const float* col, int pitch, int w, int kv, unsigned char* hi) {
   constexpr int ROWS = chunk_nodes(D) * D;
-  const float* col = raw + min(w, cw - 1) * D;
-  const int pitch = cw * D;
-#pragma unroll 2
-  for (int k0 = 8 * half; k0 < ROWS; k0 += 16) {
-    if (k0 >= kv) break;
-    float v[8], h[8];
-    read8<D>(col, pitch, k0, w < cw ? kv : 0, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = rn_tf32(v[i]), v[i] = rn_tf32(v[i] - h[i]);
+  for (int k0 = 8 * HALF; k0 < ROWS; k0 += 16) {
+    if (!WHOLE && k0 >= kv) break;
+    float v[8], h[8];
+    read8<D, WHOLE>(col, pitch, k0, kv, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tf32_split<SPLIT>(v[i], h[i], v[i]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int j = k0 / 4 + i;  // 16-byte column of the tile
@@ -216,23 +194,54 @@ __device__ __forceinline__ void convert_b(const float* raw, int w, int half, int
     }
   }
 }
+// one chunk of an operand; whole chunks without a test per row.  Columns of B behind
+// the channels repeat the last one: what they give is not stored.
+template <int D, bool SPLIT>
+__device__ __forceinline__ void chunk_a(const float* raw, int u, int cu, int kv, uint32_t ta) {
+  const float* col = raw + min(u, cu - 1) * D;
+  if (kv == chunk_nodes(D) * D)
+    convert_a<D, SPLIT, true>(col, cu * D, kv, ta);
+  else
+    convert_a<D, SPLIT, false>(col, cu * D, kv, ta);
+}
+template <int D, bool SPLIT>
+__device__ __forceinline__ void chunk_b(const float* raw, int t, int cw, int kv, unsigned char* hi) {
+  const int w = t & 63;
+  const float* col = raw + min(w, cw - 1) * D;
+  if (kv == chunk_nodes(D) * D) {
+    if (t < 64)
+      convert_b<D, SPLIT, true, 0>(col, cw * D, w, kv, hi);
+    else
+      convert_b<D, SPLIT, true, 1>(col, cw * D, w, kv, hi);
+  } else {
+    if (t < 64)
+      convert_b<D, SPLIT, false, 0>(col, cw * D, w, kv, hi);
+    else
+      convert_b<D, SPLIT, false, 1>(col, cw * D, w, kv, hi);
+  }
+}
 
-template <bool SPLIT>
+template <bool SPLIT, int VEC>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_linear_grad_tc(const __grid_constant__ LinGrad P, int stages, int stage_bytes, int g_offset,
+    k_linear_grad_tc(const __grid_constant__ Params P, int stages, int stage_bytes, int g_offset,
                      float* __restrict__ part, uint64_t limit) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* sB = base;  // 2 x (hi | lo)
   unsigned char* sRaw = base + 4 * kBTile;
+  Entry* E = reinterpret_cast<Entry*>(sRaw + stages * stage_bytes);
+  int* offs = reinterpret_cast<int*>(E + P.n_entries);
   __shared__ Shared sh;
   volatile int* abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  for (int i = threadIdx.x; i < P.n_entries * int(sizeof(Entry) / 4); i += kThreads)
+    reinterpret_cast<int*>(E)[i] = reinterpret_cast<const int*>(P.e)[i];
+  load_offsets(offs, P.offsets, P.T, P.N);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.full[s], kCopy);
       mbar_init(&sh.empty[s], 256);
     }
     for (int i = 0; i < 2; ++i) {
@@ -243,58 +252,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sh.fin, 1);
     sh.abort = 0;
-    sh.start_t = sh.start_j = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 13) tmem_alloc(&sh.tmem, kTmemCols);
-  count_chunks(P, sh.total);
+  if (warp == 15) tmem_alloc(&sh.tmem, kTmemCols);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = sh.tmem;
-  const int64_t total = total_cost(P, sh.total);
-  if (warp == 0) {  // the type of the CTA's first chunk
-    Walk w(P, sh, total);
-    int64_t j0;
-    if (w.next_entry(&j0)) {
-      const int unit = chunk_nodes(P.p[w.p].d);
-      int carry = 0;
-      for (int t0 = 0; t0 < P.T; t0 += 32) {
-        const int t = t0 + lane;
-        int n = 0;
-        if (t < P.T) {
-          int b, e;
-          lin_group(P.offsets, P.T, P.N, t, &b, &e);
-          n = (e - b + unit - 1) / unit;
-        }
-        int s = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, s, o);
-          if (lane >= o) s += v;
-        }
-        const int64_t first = int64_t(carry) + s - n;
-        if (j0 >= first && j0 < first + n) sh.start_t = t, sh.start_j = int(j0 - first);
-        carry += __shfl_sync(0xffffffffu, s, 31);
-      }
-    }
+  if (warp < 4) {
+    const int n = count_units(offs, P.T, chunk_nodes(2 * warp + 1));
+    if (lane == 0) sh.total[warp] = n;
   }
   __syncthreads();
 
-  Walk walk(P, sh, total);
+  Walk walk(P, E, offs, sh.total);
   Piece q;
   bool ok = true;
   int ci = 0;  // chunks so far
   if (warp < 8) {
     // ---- operands ----
     const bool is_a = warp < 4;
-    const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemA;
     const int t = threadIdx.x & 127;
     while (ok && walk.next(&q)) {
-      const LinPath& L = P.p[q.p];
-      const int cu = min(kMT, L.ci - q.u0), cw = min(kNT, L.co - q.w0), nq = chunk_nodes(L.d);
+      const Entry& L = E[q.e];
+      const int d = L.d, cu = L.cu, cw = L.cw, nq = chunk_nodes(d);
       for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-        const int st = ci % stages, ab = ci & 1, kv = min(nq, q.nodes - n0) * L.d;
+        const int st = ci % stages, ab = ci & 1, kv = min(nq, q.nodes - n0) * d;
         if (ci >= 2 && !wait(&sh.aempty[ab], ((ci >> 1) + 1) & 1, limit, abort, 1)) ok = false;
         if (ok && !wait(&sh.full[st], (ci / stages) & 1, limit, abort, 2)) ok = false;
         if (!ok) break;
@@ -302,13 +286,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_a) {
           fence_after_sync();
           const float* rx = reinterpret_cast<const float*>(raw);
-          const uint32_t ta = lane_base + kTmemA + ab * kTmemAStage;
+          const uint32_t ta = lane_base + ab * kTmemAStage;
           if (warp * 32 < cu) {  // (rows of the product behind the channels are not stored)
-            switch (L.d) {
-              case 1: convert_a<1, SPLIT>(rx, t, cu, kv, ta); break;
-              case 3: convert_a<3, SPLIT>(rx, t, cu, kv, ta); break;
-              case 5: convert_a<5, SPLIT>(rx, t, cu, kv, ta); break;
-              default: convert_a<7, SPLIT>(rx, t, cu, kv, ta); break;
+            switch (d) {
+              case 1: chunk_a<1, SPLIT>(rx, t, cu, kv, ta); break;
+              case 3: chunk_a<3, SPLIT>(rx, t, cu, kv, ta); break;
+              case 5: chunk_a<5, SPLIT>(rx, t, cu, kv, ta); break;
+              default: chunk_a<7, SPLIT>(rx, t, cu, kv, ta); break;
             }
           }
           mbar_arrive(&sh.empty[st]);
@@ -317,11 +301,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const float* rg = reinterpret_cast<const float*>(raw + g_offset);
           unsigned char* hi = sB + ab * 2 * kBTile;
-          switch (L.d) {
-            case 1: convert_b<1, SPLIT>(rg, t & 63, t >> 6, cw, kv, hi); break;
-            case 3: convert_b<3, SPLIT>(rg, t & 63, t >> 6, cw, kv, hi); break;
-            case 5: convert_b<5, SPLIT>(rg, t & 63, t >> 6, cw, kv, hi); break;
-            default: convert_b<7, SPLIT>(rg, t & 63, t >> 6, cw, kv, hi); break;
+          switch (d) {
+            case 1: chunk_b<1, SPLIT>(rg, t, cw, kv, hi); break;
+            case 3: chunk_b<3, SPLIT>(rg, t, cw, kv, hi); break;
+            case 5: chunk_b<5, SPLIT>(rg, t, cw, kv, hi); break;
+            default: chunk_b<7, SPLIT>(rg, t, cw, kv, hi); break;
           }
           mbar_arrive(&sh.empty[st]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -335,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemD;
     int ri = 0;  // rounds so far
     while (ok && walk.next(&q)) {
-      const LinPath& L = P.p[q.p];
-      const int cu = min(kMT, L.ci - q.u0), cw = min(kNT, L.co - q.w0), nq = chunk_nodes(L.d);
+      const Entry& L = E[q.e];
+      const int cu = L.cu, cw = L.cw, nq = chunk_nodes(L.d);
       const int rounds = ((q.nodes + nq - 1) / nq + kRound - 1) / kRound;
       float acc[kNT];
 #pragma unroll
@@ -363,78 +347,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh.dempty[db]);
       }
       if (!ok || r >= cu) continue;
-      float* dst = q.slot < 0 ? P.dw + int64_t(q.t) * P.wnumel + L.woff + int64_t(q.u0 + r) * L.co + q.w0
-                              : part + (int64_t(q.slot) * kMT + r) * kNT;
+      if (q.slot >= 0) {  // a partial tile has room for all columns
+        float4* dst = reinterpret_cast<float4*>(part + (int64_t(q.slot) * kMT + r) * kNT);
 #pragma unroll
-      for (int i = 0; i < kNT; i += 4)
-        if (i < cw) *reinterpret_cast<float4*>(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-    }
-  } else if (warp == 12) {
-    // ---- node rows to shared memory ----
-    while (ok && walk.next(&q)) {
-      const LinPath& L = P.p[q.p];
-      const uint32_t bx = uint32_t(min(kMT, L.ci - q.u0) * L.d * 4), bg = uint32_t(min(kNT, L.co - q.w0) * L.d * 4);
-      const float* x = P.x + L.xoff + q.u0 * L.d;
-      const float* g = P.g + L.goff + q.w0 * L.d;
-      const int nq = chunk_nodes(L.d);
-      for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-        const int st = ci % stages, cnt = min(nq, q.nodes - n0);
-        int node[2];
+        for (int i = 0; i < kNT; i += 4) dst[i / 4] = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+      } else {
+        float* dst = P.dw + int64_t(q.t) * P.wnumel + L.woff + int64_t(r) * L.co;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int k = lane + 32 * i;
-          node[i] = k < cnt ? P.perm[q.first + n0 + k] : 0;
-          if (node[i] < 0 || node[i] >= P.N) node[i] = 0;
-        }
-        if (ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
-        ok = __all_sync(0xffffffffu, ok && !*abort);
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&sh.full[st], uint32_t(cnt) * (bx + bg));
-        __syncwarp();
-        const uint32_t dst = smem_u32(sRaw + st * stage_bytes);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int k = lane + 32 * i;
-          if (k < cnt) {
-            bulk_load(dst + k * bx, x + int64_t(node[i]) * P.dim_x, bx, &sh.full[st]);
-            bulk_load(dst + g_offset + k * bg, g + int64_t(node[i]) * P.dim_g, bg, &sh.full[st]);
+        for (int i = 0; i < kNT; i += VEC) {
+          if (i < cw) {
+            if constexpr (VEC == 4)
+              *reinterpret_cast<float4*>(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+            else
+              dst[i] = acc[i];
           }
         }
       }
     }
-    if (*abort)
-      for (int c = (ci > stages ? ci - stages : 0); c < ci; ++c)
-        if (!mbar_wait_for(&sh.full[c % stages], (c / stages) & 1, kDrainLimitNs)) break;
+  } else if (warp < 15) {
+    // ---- node rows to shared memory, several chunks ahead ----
+    const int r = threadIdx.x - 384;
+    while (walk.next(&q)) {  // (a warp that gave up keeps passing the group's barriers)
+      const Entry& L = E[q.e];
+      const int d = L.d, nq = chunk_nodes(d), lx = L.cu * d, lg = L.cw * d;
+      const float *x = P.x + L.xoff, *g = P.g + L.goff;
+      // the nodes of the next chunk are read while this one is copied
+      int node = r < min(nq, q.nodes) ? P.perm[q.first + r] : 0;
+      for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
+        const int st = ci % stages, cnt = min(nq, q.nodes - n0);
+        int* nodes = sh.node[ci & 1];
+        if (r < 64) nodes[r] = (node >= 0 && node < P.N) ? node : 0;
+        asm volatile("bar.sync 1, 96;" ::: "memory");
+        node = r < nq && n0 + nq + r < q.nodes ? P.perm[q.first + n0 + nq + r] : 0;
+        if (ok && ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
+        if (!ok) continue;
+        const uint32_t dst = smem_u32(sRaw + st * stage_bytes);
+#pragma unroll 4
+        for (Pieces<VEC> p(cnt, lx, r, kCopy); p.valid(); p.advance())
+          copy_async<VEC>(dst + p.i * (4 * VEC), x + int64_t(nodes[p.q]) * P.dim_x + p.o * VEC);
+#pragma unroll 4
+        for (Pieces<VEC> p(cnt, lg, r, kCopy); p.valid(); p.advance())
+          copy_async<VEC>(dst + g_offset + p.i * (4 * VEC), g + int64_t(nodes[p.q]) * P.dim_g + p.o * VEC);
+        copies_arrive(&sh.full[st]);
+      }
+    }
+    copies_wait_all();  // no copy may be in flight when the CTA ends
   } else {
     // ---- MMAs ----
     int ri = 0;
     while (ok && walk.next(&q)) {
-      const LinPath& L = P.p[q.p];
-      const int cw = min(kNT, L.co - q.w0), nq = chunk_nodes(L.d);
-      const uint32_t idesc = idesc_tf32(kMT, (cw + 15) & ~15);
+      const Entry& L = E[q.e];
+      const int d = L.d, nq = chunk_nodes(d);
+      const uint32_t idesc = idesc_tf32(kMT, (L.cw + 15) & ~15);
       int in_round = 0;
       for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-        const int ab = ci & 1, db = ri & 1, steps = (min(nq, q.nodes - n0) * L.d + 7) / 8;
+        const int ab = ci & 1, db = ri & 1, steps = (min(nq, q.nodes - n0) * d + 7) / 8;
         if (in_round == 0 && ri >= 2 && !wait(&sh.dempty[db], ((ri >> 1) + 1) & 1, limit, abort, 5)) ok = false;
         if (ok && !wait(&sh.afull[ab], (ci >> 1) & 1, limit, abort, 6)) ok = false;
         if (!ok) break;
         fence_after_sync();
         const bool last = ++in_round == kRound || n0 + nq >= q.nodes;
         if (lane == 0) {
-          const uint32_t td = tmem + kTmemD + db * kNT;
-          const uint32_t ah = tmem + kTmemA + ab * kTmemAStage, al = ah + kKMax;
-          const uint32_t bh = smem_u32(sB + ab * 2 * kBTile), bl = bh + kBTile;
-          auto off = [](int k) { return uint32_t((k >> 2) * (kNT * 128) + (k & 3) * 32); };
+          const uint32_t td = tmem + kTmemD + db * kNT, a = tmem + kTmemA + ab * kTmemAStage;
+          const uint64_t bh = sw128_kmajor(smem_u32(sB + ab * 2 * kBTile)),
+                         bl = sw128_kmajor(smem_u32(sB + ab * 2 * kBTile + kBTile));
+          auto step = [](int k) { return uint64_t((k >> 2) * (kNT * 128 / 16) + (k & 3) * 2); };
           uint32_t acc = in_round > 1;
-          if (SPLIT)
-            for (int k = 0; k < steps; ++k) {
-              mma_tf32_ta(td, al + 8 * k, sw128_kmajor(bh + off(k)), idesc, acc);
-              acc = 1;
-              mma_tf32_ta(td, ah + 8 * k, sw128_kmajor(bl + off(k)), idesc, 1);
+          if (SPLIT) {
+#pragma unroll
+            for (int k = 0; k < kKMax / 8; ++k) {
+              if (k >= steps) break;
+              mma_tf32_ta(td, a + kKMax + 8 * k, bh + step(k), idesc, k > 0 ? 1u : acc);
+              mma_tf32_ta(td, a + 8 * k, bl + step(k), idesc, 1);
             }
-          for (int k = 0; k < steps; ++k) {
-            mma_tf32_ta(td, ah + 8 * k, sw128_kmajor(bh + off(k)), idesc, acc);
             acc = 1;
+          }
+#pragma unroll
+          for (int k = 0; k < kKMax / 8; ++k) {
+            if (k >= steps) break;
+            mma_tf32_ta(td, a + 8 * k, bh + step(k), idesc, k > 0 ? 1u : acc);
           }
           mma_commit(&sh.aempty[ab]);
           if (last) mma_commit(&sh.dfull[db]);
@@ -451,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == 15) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -461,73 +452,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 // for a type without nodes, the sum of the partial tiles in CTA order for one whose
 // rows are spread over several shares, nothing otherwise.
 constexpr int kJoinRows = 16;
-__global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant__ LinGrad P, int ctas,
+__global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant__ Params P, int ctas,
                                                           const float* __restrict__ part) {
-  __shared__ int total[4];
-  __shared__ int s_before, s_n;
-  count_chunks(P, total);
-  const int t = blockIdx.x % P.T;
-  int e = blockIdx.x / P.T, p = 0;
-  while (e >= tiles_u(P.p[p]) * tiles_w(P.p[p])) e -= tiles_u(P.p[p]) * tiles_w(P.p[p]), ++p;
-  const LinPath& L = P.p[p];
-  const int u0 = e / tiles_w(L) * kMT, w0 = e % tiles_w(L) * kNT;
-  const int cu = min(kMT, L.ci - u0), cw = min(kNT, L.co - w0);
-  if (threadIdx.x >= 128 && threadIdx.x < 160) {  // chunks of the types before t, and of t
-    const int lane = threadIdx.x & 31, unit = chunk_nodes(L.d);
-    int before = 0, n = 0;
-    for (int k = lane; k <= t; k += 32) {
-      int b, g;
-      lin_group(P.offsets, P.T, P.N, k, &b, &g);
-      const int c = (g - b + unit - 1) / unit;
-      if (k < t) before += c;
-      else n = c;
-    }
-    before = __reduce_add_sync(0xffffffffu, before);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) s_before = before, s_n = n;
+  __shared__ int offs[TPCONV_MAX_TYPES + 2];
+  __shared__ int total[4], s_slots, slot[kSMs];
+  const int t = blockIdx.x % P.T, e = blockIdx.x / P.T, warp = threadIdx.x >> 5;
+  const Entry& L = P.e[e];
+  load_offsets(offs, P.offsets, P.T, P.N);
+  __syncthreads();
+  if (warp < 4) {
+    const int n = count_units(offs, P.T, chunk_nodes(2 * warp + 1));
+    if ((threadIdx.x & 31) == 0) total[warp] = n;
   }
   __syncthreads();
-  const int n = s_n;
-  float* dw = P.dw + int64_t(t) * P.wnumel + L.woff + int64_t(u0) * L.co + w0;
-  const int r0 = blockIdx.y * kJoinRows, r1 = min(cu, r0 + kJoinRows);
-  int b0 = 0, b1 = -1;
-  int64_t all = 0, seg = 0;
-  const int c = chunk_cost(L, u0, w0);
-  if (n > 0) {
-    all = total_cost(P, total);
-    int64_t begin = 0;  // cost before the entry
-    for (int k = 0; k <= p; ++k)
-      for (int u = 0; u < tiles_u(P.p[k]); ++u)
-        for (int w = 0; w < tiles_w(P.p[k]); ++w)
-          if (k < p || u * kMT < u0 || (u * kMT == u0 && w * kNT < w0))
-            begin += int64_t(total[P.p[k].d >> 1]) * chunk_cost(P.p[k], u * kMT, w * kNT);
-    seg = begin + int64_t(s_before) * c;
-    // the share that holds the chunk whose cost begins at x
-    auto owner = [&](int64_t x) {
-      int b = int(x * ctas / all);
-      while (b > 0 && x < share_begin(all, b, ctas)) --b;
-      while (b + 1 < ctas && x >= share_begin(all, b + 1, ctas)) ++b;
-      return b;
-    };
-    b0 = owner(seg);
-    b1 = owner(seg + int64_t(n - 1) * c);
-    if (b0 == b1) return;
+  const int r0 = blockIdx.y * kJoinRows, r1 = min(L.cu, r0 + kJoinRows), cw = L.cw;
+  if (r0 >= r1) return;
+  if (warp == 0) {
+    // the slots of the type's pieces
+    const int unit = chunk_nodes(L.d), n = group_units(offs, t, unit), c = L.cost;
+    int m = -1;
+    if (n == 0) {
+      m = 0;
+    } else {
+      const int64_t all = total_cost(P, total);
+      int64_t seg = int64_t(count_units(offs, t, unit)) * c;  // cost before the type's first chunk
+      for (int k = 0; k < e; ++k) seg += int64_t(total[P.e[k].d >> 1]) * P.e[k].cost;
+      const int64_t end = seg + int64_t(n - 1) * c;  // cost before its last chunk
+      m = 0;
+      for (int b0 = 0; b0 < ctas; b0 += 32) {
+        const int b = b0 + threadIdx.x;
+        bool has = false, first = false;
+        if (b < ctas) {
+          const int64_t lo = share_begin(all, b, ctas), hi = share_begin(all, b + 1, ctas);
+          first = lo <= seg && seg < hi;
+          // the first chunk of the type at or behind lo, if it is in the share
+          const int64_t x = lo <= seg ? seg : seg + div_cost(lo - seg + c - 1, c) * c;
+          has = x <= end && x < hi;
+        }
+        const unsigned mask = __ballot_sync(0xffffffffu, has);
+        if (has) slot[m + __popc(mask & ((1u << threadIdx.x) - 1))] = 2 * b + first;
+        m += __popc(mask);
+      }
+      if (m == 1) m = -1;  // all in one share: stored by its CTA
+    }
+    if (threadIdx.x == 0) s_slots = m;
   }
+  __syncthreads();
+  const int m = s_slots;
+  if (m < 0) return;
+  float* dw = P.dw + int64_t(t) * P.wnumel + L.woff;
   for (int i = threadIdx.x; i < (r1 - r0) * cw; i += 256) {
     const int r = r0 + i / cw, w = i % cw;
+    const float* p0 = part + int64_t(r) * kNT + w;
     float s = 0.f;
-    for (int b = b0; b <= b1; ++b) {
-      if (b > b0) {  // a share narrower than a chunk's cost may hold none
-        const int64_t k = (share_begin(all, b, ctas) - seg + c - 1) / c;
-        if (seg + k * c >= share_begin(all, b + 1, ctas)) continue;
-      }
-      s += part[(int64_t(b == b0 ? 2 * b + 1 : 2 * b) * kMT + r) * kNT + w];
-    }
+#pragma unroll 8
+    for (int b = 0; b < m; ++b) s += p0[int64_t(slot[b]) * kMT * kNT];
     dw[int64_t(r) * L.co + w] = s;
   }
 }
 
-constexpr int kSMs = 148;
+int tiles_u(const LinPath& p) { return (p.ci + kMT - 1) / kMT; }
+int tiles_w(const LinPath& p) { return (p.co + kNT - 1) / kNT; }
 
 // one CTA per SM, or per chunk where there are fewer (an upper bound)
 int ctas_of(const LinPath* path, int n, int T, int64_t N) {
@@ -537,17 +522,21 @@ int ctas_of(const LinPath* path, int n, int T, int64_t N) {
   return int(std::max<int64_t>(1, std::min<int64_t>(kSMs, c)));
 }
 
+bool vec4(const LinGrad& G) {
+  const auto bad = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; };
+  if (G.dim_x % 4 || G.dim_g % 4 || G.wnumel % 4 || bad(G.x) || bad(G.g) || bad(G.dw)) return false;
+  for (int p = 0; p < G.n_paths; ++p) {
+    const LinPath& L = G.p[p];
+    if (L.ci % 4 || L.co % 4 || L.xoff % 4 || L.goff % 4 || L.woff % 4) return false;
+  }
+  return true;
+}
+
 }  // namespace
 
 bool linear_grad_tc_supported(const LinGrad& G) {
-  const auto bad = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; };
-  if (G.dim_x % 4 || G.dim_g % 4 || bad(G.x) || bad(G.g) || bad(G.dw)) return false;
   int entries = 0;
-  for (int p = 0; p < G.n_paths; ++p) {
-    const LinPath& L = G.p[p];
-    if (L.ci % 4 || L.co % 4 || L.xoff % 4 || L.goff % 4) return false;
-    entries += tiles_u(L) * tiles_w(L);
-  }
+  for (int p = 0; p < G.n_paths; ++p) entries += tiles_u(G.p[p]) * tiles_w(G.p[p]);
   return entries <= kLinGradTcEntries;
 }
 
@@ -556,25 +545,41 @@ size_t linear_grad_tc_bytes(const LinPath* path, int n, int T, int64_t N) {
 }
 
 cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t limit, cudaStream_t st) {
-  int sx = 0, sg = 0, entries = 0;
+  Params P;
+  std::memset(&P, 0, sizeof(P));
+  P.T = G.T, P.dim_x = G.dim_x, P.dim_g = G.dim_g, P.N = G.N, P.wnumel = G.wnumel;
+  P.x = G.x, P.g = G.g, P.dw = G.dw, P.perm = G.perm, P.offsets = G.offsets;
+  int sx = 0, sg = 0;
   for (int p = 0; p < G.n_paths; ++p) {
     const LinPath& L = G.p[p];
-    sx = std::max(sx, std::min(kMT, L.ci) * L.d * chunk_nodes(L.d) * 4);
-    sg = std::max(sg, std::min(kNT, L.co) * L.d * chunk_nodes(L.d) * 4);
-    entries += tiles_u(L) * tiles_w(L);
+    for (int u0 = 0; u0 < L.ci; u0 += kMT)
+      for (int w0 = 0; w0 < L.co; w0 += kNT) {
+        Entry& E = P.e[P.n_entries++];
+        E.d = L.d, E.xoff = L.xoff + u0 * L.d, E.goff = L.goff + w0 * L.d;
+        E.cu = std::min(kMT, L.ci - u0), E.cw = std::min(kNT, L.co - w0), E.co = L.co;
+        E.woff = L.woff + int64_t(u0) * L.co + w0;
+        // the KB that a chunk moves, at least the rows that it converts
+        E.cost = 8 + std::max((E.cu + E.cw) * L.d * chunk_nodes(L.d) / 256, L.d * chunk_nodes(L.d) / 4);
+        P.coef[L.d >> 1] += E.cost;
+        sx = std::max(sx, E.cu * L.d * chunk_nodes(L.d) * 4);
+        sg = std::max(sg, E.cw * L.d * chunk_nodes(L.d) * 4);
+      }
   }
-  const int stage = (sx + sg + 127) & ~127;
-  const int room = kSMemMax - 1024 - int(sizeof(Shared)) - 256 - 4 * kBTile;
-  const int stages = std::min(kMaxStages, room / stage);
+  sx = (sx + 15) & ~15;
+  const int stage = (sx + sg + 15) & ~15;
+  const int fixed = 1024 + 4 * kBTile + P.n_entries * int(sizeof(Entry)) + (P.T + 2) * 4;
+  const int stages = std::min(kMaxStages, (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / stage);
   if (stages < 2) return cudaErrorInvalidValue;
-  const int sm = 1024 + 4 * kBTile + stages * stage;
-  auto* k = split ? k_linear_grad_tc<true> : k_linear_grad_tc<false>;
+  const int sm = fixed + stages * stage;
+  const bool v = vec4(G);
+  auto* k = split ? (v ? k_linear_grad_tc<true, 4> : k_linear_grad_tc<true, 1>)
+                  : (v ? k_linear_grad_tc<false, 4> : k_linear_grad_tc<false, 1>);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
   if (e) return e;
   const int ctas = ctas_of(G.p, G.n_paths, G.T, G.N);
-  k<<<ctas, kThreads, sm, st>>>(G, stages, stage, sx, part, limit);
+  k<<<ctas, kThreads, sm, st>>>(P, stages, stage, sx, part, limit);
   if ((e = cudaGetLastError())) return e;
-  k_linear_grad_join<<<dim3(unsigned(entries * G.T), kMT / kJoinRows), 256, 0, st>>>(G, ctas, part);
+  k_linear_grad_join<<<dim3(unsigned(P.n_entries * G.T), kMT / kJoinRows), 256, 0, st>>>(P, ctas, part);
   return cudaGetLastError();
 }
 

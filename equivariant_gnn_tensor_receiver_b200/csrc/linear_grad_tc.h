@@ -5,9 +5,9 @@
 
 namespace tpc {
 
-constexpr int kLinGradTcEntries = 64;  // (path, channel tile) pairs of a call
+constexpr int kLinGradTcEntries = 48;  // (path, channel tile) pairs of a call
 
-// whether every block and tensor can be copied 16 bytes at a time
+// whether the call's list of (path, channel tile) pairs fits
 bool linear_grad_tc_supported(const LinGrad& G);
 // bytes of the partial tiles of a call
 size_t linear_grad_tc_bytes(const LinPath* path, int n, int T, int64_t N);

@@ -6,9 +6,9 @@
 namespace tpc {
 
 constexpr int kLinTcChunks = 4;    // 64-channel chunks of a resident weight: up to 256 source channels
-constexpr int kLinTcEntries = 64;  // (output block, 64 columns) pairs of a call
+constexpr int kLinTcEntries = 48;  // (output block, 64 columns) pairs of a call
 
-// whether every block and tensor of the product can be copied 16 bytes at a time and its weights stay resident
+// whether the weights of every (block, columns, type) stay resident
 bool linear_tc_supported(const LinRows& R);
 // the row product; split = 3xTF32, else one TF32 pass
 cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStream_t st);

@@ -34,16 +34,58 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// untiled bulk copies: both addresses and the size are multiples of 16 bytes
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+// TF32 halves of a: hi = a rounded to nearest (ties away from zero), lo = the exact
+// remainder, of which the tensor core reads the first 11 bits.  By integer
+// arithmetic: the conversion instruction runs at a quarter of the rate, and two a
+// value were what bounded the kernels.  (Infinities and NaN end as NaN through lo.)
+__device__ __forceinline__ float tf32_hi(float a) {
+  return __uint_as_float((__float_as_uint(a) + 0x1000u) & 0xffffe000u);
 }
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-               : "memory");
+// hi (and lo) of one operand value: SPLIT as above, else the value rounded to TF32
+template <bool SPLIT>
+__device__ __forceinline__ void tf32_split(float a, float& hi, float& lo) {
+  if constexpr (SPLIT) {
+    hi = tf32_hi(a);
+    lo = a - hi;
+  } else {
+    hi = rn_tf32(a);
+    lo = 0.f;
+  }
 }
+
+// asynchronous copies of VEC floats to shared memory, and their arrival on a barrier
+template <int VEC>
+__device__ __forceinline__ void copy_async(uint32_t dst, const float* src) {
+  if constexpr (VEC == 4)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Pieces of VEC floats of `rows` rows of `len` floats, dealt out to `threads`
+// threads in order: piece i is row q, offset o of that row.
+template <int VEC>
+struct Pieces {
+  int q, o, n, dq, dr, total, i, step;
+  __device__ __forceinline__ Pieces(int rows, int len, int thread, int threads) {
+    n = len / VEC;
+    total = rows * n;
+    i = thread, step = threads;
+    q = thread / n, o = thread - q * n;
+    dq = threads / n, dr = threads - dq * n;
+  }
+  __device__ __forceinline__ bool valid() const { return i < total; }
+  __device__ __forceinline__ void advance() {
+    i += step;
+    q += dq;
+    o += dr;
+    if (o >= n) o -= n, ++q;
+  }
+};
 
 __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
   uint32_t ok;
@@ -76,6 +118,58 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* b, uint32_t parity, uint
     }
   }
   return __all_sync(0xffffffffu, ok);
+}
+
+// ---- ragged groups ---------------------------------------------------------------
+// offs[0 .. T + 1] in shared memory: where each group begins (clamped to [0, N]), N at
+// the end; group T holds the nodes without a type.
+__device__ __forceinline__ void load_offsets(int* offs, const int* offsets, int T, int64_t N) {
+  for (int t = threadIdx.x; t <= T + 1; t += blockDim.x)
+    offs[t] = t <= T ? min(max(offsets[t], 0), int(N)) : int(N);
+}
+__device__ __forceinline__ int group_units(const int* offs, int t, int unit) {
+  const int n = offs[t + 1] - offs[t];
+  return n > 0 ? (n + unit - 1) / unit : 0;
+}
+// units of the first `groups` groups; one warp, the same answer in every lane
+__device__ __forceinline__ int count_units(const int* offs, int groups, int unit) {
+  int s = 0;
+  for (int t = threadIdx.x & 31; t < groups; t += 32) s += group_units(offs, t, unit);
+  return __reduce_add_sync(0xffffffffu, s);
+}
+// the group of unit `at`, and its index there
+__device__ __forceinline__ void seek_unit(const int* offs, int groups, int unit, int64_t at, int* t, int* j) {
+  const int lane = threadIdx.x & 31;
+  int64_t carry = 0;
+  *t = groups, *j = 0;
+  for (int t0 = 0; t0 < groups; t0 += 32) {
+    const int n = t0 + lane < groups ? group_units(offs, t0 + lane, unit) : 0;
+    int s = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    const int64_t first = carry + s - n;
+    const unsigned hit = __ballot_sync(0xffffffffu, at >= first && at < first + n);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      *t = t0 + src;
+      *j = int(at - __shfl_sync(0xffffffffu, first, src));
+      return;
+    }
+    carry += __shfl_sync(0xffffffffu, s, 31);
+  }
+}
+
+// non-negative division; 32-bit where the operands fit
+__device__ __forceinline__ int64_t div_cost(int64_t a, int b) {
+  return a <= 0xffffffffll ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+// the first cost of share b of `shares` equal ones
+__device__ __forceinline__ int64_t share_begin(int64_t total, int b, int shares) {
+  const int64_t q = div_cost(total, shares);
+  return q * b + min(int64_t(b), total - q * shares);
 }
 
 }  // namespace tc
