@@ -13,10 +13,11 @@
 //   them (3xTF32, Ootomo & Yokota, 2022) and store hi and lo as the A operand in
 //   TMEM: the transposition from [channel][m] to rows costs one shared-memory read
 //   per element and no write;
-//   one thread issues D += A_lo B_hi + A_hi B_lo, then A_hi B_hi (the small products
-//   first, while the accumulator is small);
-//   epilogue threads, one per row, lay D out as [channel][m] in shared memory, and
-//   store the nodes' pieces, 16 bytes a thread.
+//   one thread issues, 8 channels a step, (D1 | D2) += A_hi (B_hi | B_lo) as one product
+//   of up to 128 columns, and D2 += A_lo B_hi: two instructions instead of three, and
+//   the small products add up among themselves;
+//   epilogue threads, one per row and 32 columns, lay D1 + D2 out as [channel][m] in
+//   shared memory, and store the nodes' pieces, 16 bytes a thread.
 // The pitch of a node in shared memory is 4 or 8 floats off a multiple of 32, which
 // leaves at most two rows of a warp on a bank.
 //
@@ -27,8 +28,10 @@
 //
 // One persistent CTA per SM takes an equal share of the (block, columns) x types x
 // tiles list, in order, so that its weight changes rarely; the group sizes are read
-// from the device.  Warps 0-3 convert, 4-7 run the epilogue, 8-11 copy, 12 issues the
-// MMAs.  (Bulk copies of a node's piece were tried in place of the copy threads: about
+// from the device.  Warps 0-7 convert (two per 32 rows, 32 channels each), 8-15 run the
+// epilogue (two per 32 rows, 32 columns each), 16-19 copy, 20 issues the MMAs: with one
+// warpgroup for each role their latencies, not the issue slots (36 % busy), bounded
+// the tile.  (Bulk copies of a node's piece were tried in place of the copy threads: about
 // 60 cycles of issue a copy, 2.5 times the time at 64 scalars a node.)
 // Every wait is bounded by the call's limit; on expiry the kernel records it, stops
 // issuing, waits (bounded) for its own copies and MMAs, frees TMEM and returns.
@@ -51,14 +54,16 @@ __device__ int g_linear_error;  // first code recorded by an expired wait (0 = n
 constexpr int kSMs = 148;
 constexpr int kNT = 64, kKC = 64;             // columns of a tile, channels of a chunk
 constexpr int kMaxChunks = kLinTcChunks;      // chunks of a resident weight
-constexpr int kWHalf = kNT * kKC * 4;         // hi or lo of one chunk: 16 KB
+// one chunk of a weight: 32 channels behind 32 channels, each the rows of up to 64 output
+// channels' hi and behind them their lo, 128 bytes a row (K-major, 128-byte swizzle)
+constexpr int kWHalf = 2 * kNT * 32 * 4;
 constexpr int kWChunk = 2 * kWHalf;
 constexpr int kRaw = 32928;                   // a raw chunk or an output tile (see node_pitch)
 constexpr int kMaxStages = 4;
 constexpr int kSMemMax = 227 * 1024;
-constexpr int kThreads = 416;
+constexpr int kThreads = 672;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemA = 0, kTmemAStage = 128, kTmemD = 256;  // A: 2 x (hi 64 | lo 64), D: 2 x 64
+constexpr uint32_t kTmemA = 0, kTmemAStage = 128, kTmemD = 256, kTmemDStage = 128;  // A: 2 x (hi 64 | lo 64), D: 2 x (D1 | D2)
 
 // nodes of a tile; floats of a node's 64 channels plus padding (multiple of 4)
 __host__ __device__ constexpr int tile_of(int d) { return d == 1 ? 120 : 128 / d; }
@@ -117,9 +122,11 @@ struct Walk {
   const int* offs;
   const int* total;
   int n_entries, T;
-  int64_t lo, hi, base = 0, left = 0;
-  int e = -1, unit = 1, t = 0, j = 0, tiles = 0;
-  bool fresh = true;
+  int64_t lo, hi, base = 0;
+  int left = 0;                // tiles of this share left in the entry
+  int e = -1, unit = 1, t = 0;
+  int at = 0, end = 0;         // the group's next node, its end
+  bool fresh = true, empty = false;
 
   __device__ Walk(const Params& P, const Entry* entries, const int* o, const int* tot)
       : E(entries), offs(o), total(tot), n_entries(P.n_entries), T(P.T) {
@@ -129,41 +136,45 @@ struct Walk {
     lo = share_begin(c, blockIdx.x, gridDim.x);
     hi = share_begin(c, blockIdx.x + 1, gridDim.x);
   }
-  __device__ bool next(Item* it) {
-    if (left == 0) {
-      for (;;) {
-        if (e >= 0) base += int64_t(total[E[e].d >> 1]) * E[e].cost;
-        if (++e >= n_entries || base >= hi) {
-          e = n_entries;
-          return false;
-        }
-        const int c = E[e].cost;
-        const int64_t n = total[E[e].d >> 1];
-        const int64_t a = lo <= base ? 0 : min(div_cost(lo - base + c - 1, c), n),
-                      b = min(div_cost(hi - base + c - 1, c), n);
-        if (a < b) {
-          left = b - a;
-          unit = tile_of(E[e].d);
-          seek_unit(offs, T + 1, unit, a, &t, &j);
-          tiles = t <= T ? group_units(offs, t, unit) : 0;
-          fresh = true;
-          break;
-        }
+  __device__ bool next_entry() {
+    for (;;) {
+      if (e >= 0) base += int64_t(total[E[e].d >> 1]) * E[e].cost;
+      if (++e >= n_entries || base >= hi) {
+        e = n_entries;
+        return false;
+      }
+      const int c = E[e].cost;
+      const int64_t n = total[E[e].d >> 1];
+      const int64_t a = lo <= base ? 0 : min(div_cost(lo - base + c - 1, c), n),
+                    b = min(div_cost(hi - base + c - 1, c), n);
+      if (a < b) {
+        left = int(b - a);
+        unit = tile_of(E[e].d);
+        empty = E[e].count == 0;
+        int j;
+        seek_unit(offs, T + 1, unit, a, &t, &j);
+        end = t <= T ? offs[t + 1] : 0;
+        at = t <= T ? offs[t] + j * unit : 0;
+        fresh = true;
+        return true;
       }
     }
-    while (j >= tiles) {
+  }
+  __device__ bool next(Item* it) {
+    if (left == 0 && !next_entry()) return false;
+    while (at >= end) {
       if (t >= T) return false;
-      ++t, j = 0, fresh = true;
-      tiles = group_units(offs, t, unit);
+      ++t, fresh = true;
+      at = offs[t], end = offs[t + 1];
     }
     it->e = e, it->t = t;
-    it->first = offs[t] + j * unit;
-    it->count = min(unit, offs[t + 1] - it->first);
+    it->first = at;
+    it->count = min(unit, end - at);
     it->run = fresh;
-    it->zero = t >= T || E[e].count == 0;
+    it->zero = empty || t >= T;
     fresh = false;
-    ++j, --left;
-    it->run_last = left == 0 || j >= tiles;
+    at += unit, --left;
+    it->run_last = left == 0 || at >= end;
     return true;
   }
 };
@@ -195,28 +206,36 @@ __device__ __forceinline__ void convert16(const float* row, int k0, int kc, uint
   tmem_st16(ta + k0, h);
   if (SPLIT) tmem_st16(ta + kKC + k0, v);
 }
-// one chunk of the thread's row: raw -> hi (and lo) in TMEM
+// 32 channels of one chunk of the thread's row: raw -> hi (and lo) in TMEM
 template <int D, bool SPLIT>
-__device__ __forceinline__ void convert(const float* raw, int r, int kc, uint32_t ta) {
+__device__ __forceinline__ void convert(const float* raw, int r, int first, int kc, uint32_t ta) {
   constexpr int ROWS = tile_of(D) * D;
   const int rr = r < ROWS ? r : ROWS - 1;
   const float* row = raw + (rr / D) * node_pitch(D) + rr % D;
-  if (kc == kKC) {
 #pragma unroll
-    for (int k0 = 0; k0 < kKC; k0 += 16) convert16<D, SPLIT, true>(row, k0, kc, ta);
-  } else {
-    for (int k0 = 0; k0 < kc; k0 += 16) convert16<D, SPLIT, false>(row, k0, kc, ta);
+  for (int i = 0; i < 32; i += 16) {
+    if (first + i + 16 <= kc)
+      convert16<D, SPLIT, true>(row, first + i, kc, ta);
+    else if (first + i < kc)
+      convert16<D, SPLIT, false>(row, first + i, kc, ta);
   }
 }
-template <int D>
-__device__ __forceinline__ void lay_out(uint32_t td, float* stage, int r, int nw) {
+template <int D, bool SPLIT>
+__device__ __forceinline__ void lay_out(uint32_t td, float* stage, int r, int first, int nw) {
   constexpr int ROWS = tile_of(D) * D;
   float* row = stage + (r / D) * node_pitch(D) + r % D;
 #pragma unroll
-  for (int c = 0; c < kNT; c += 16) {
+  for (int i = 0; i < 32; i += 16) {
+    const int c = first + i;
     if (c >= nw) break;
     float v[16];
     tmem_ld16(td + c, v);
+    if (SPLIT) {
+      float w[16];
+      tmem_ld16(td + ((nw + 15) & ~15) + c, w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] += w[i];
+    }
     if (r < ROWS) {
       if constexpr (D == 1) {
 #pragma unroll
@@ -227,19 +246,6 @@ __device__ __forceinline__ void lay_out(uint32_t td, float* stage, int r, int nw
         for (int i = 0; i < 16; ++i) row[(c + i) * D] = v[i];
       }
     }
-  }
-}
-
-// one chunk's products: 8 channels a step, each operand's hi and lo
-__device__ __forceinline__ void issue(uint32_t td, uint32_t a, uint64_t bh, uint64_t bl, uint32_t idesc, int k,
-                                      uint32_t acc, bool cross) {
-  // (the descriptors' address field counts 16 bytes: 32 bytes a step, 8 KB behind 32 channels)
-  const uint64_t step = uint64_t((k >> 2) * (kNT * 128 / 16) + (k & 3) * 2);
-  if (cross) {
-    mma_tf32_ta(td, a + kKC + 8 * k, bh + step, idesc, acc);
-    mma_tf32_ta(td, a + 8 * k, bl + step, idesc, 1);
-  } else {
-    mma_tf32_ta(td, a + 8 * k, bh + step, idesc, acc);
   }
 }
 
@@ -268,21 +274,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sh.full[s], 128);
-      mbar_init(&sh.empty[s], 128);
+      mbar_init(&sh.empty[s], 256);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.afull[i], 128);
+      mbar_init(&sh.afull[i], 256);
       mbar_init(&sh.aempty[i], 1);
       mbar_init(&sh.dfull[i], 1);
-      mbar_init(&sh.dempty[i], 128);
+      mbar_init(&sh.dempty[i], 256);
     }
-    mbar_init(&sh.wfull, 256);
+    mbar_init(&sh.wfull, 512);
     mbar_init(&sh.wfree, 1);
     mbar_init(&sh.fin, 1);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) tmem_alloc(&sh.tmem, kTmemCols);
+  if (warp == 20) tmem_alloc(&sh.tmem, kTmemCols);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item it;
   // the weight of a run, by the converter and epilogue threads: thread (n, q0) takes four channels at a time
   auto load_weight = [&](const Entry& O, int t) {
-    const int n = threadIdx.x & 63;
+    const int n = threadIdx.x & 63, n16 = (O.nw + 15) & ~15;
     int c = 0;
     for (int s = 0; s < O.count; ++s) {
       const LinSource& Q = S[O.first + s];
@@ -305,23 +311,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k0 = 0; k0 < Q.k; k0 += kKC, ++c) {
         unsigned char* hi = sW + c * kWChunk;
         const int kc = min(kKC, Q.k - k0);
-        float v[4][4];
+        float v[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            const int k = 4 * (int(threadIdx.x >> 6) + 4 * i) + f;
+            const int k = 4 * (int(threadIdx.x >> 6) + 8 * i) + f;
             v[i][f] = (n < O.nw && k < kc) ? __ldg(w + int64_t(k0 + k) * Q.rk) : 0.f;
           }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int q = (threadIdx.x >> 6) + 4 * i;
+        for (int i = 0; i < 2; ++i) {
+          const int q = (threadIdx.x >> 6) + 8 * i;
           float h[4], l[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) tf32_split<SPLIT>(v[i][f], h[f], l[f]);
-          const int off = (q >> 3) * (kNT * 128) + n * 128 + (((q & 7) ^ (n & 7)) << 4);
-          *reinterpret_cast<float4*>(hi + off) = make_float4(h[0], h[1], h[2], h[3]);
-          if (SPLIT) *reinterpret_cast<float4*>(hi + kWHalf + off) = make_float4(l[0], l[1], l[2], l[3]);
+          // (the lo rows begin at a multiple of 16: the same swizzle)
+          const int off = (q >> 3) * kWHalf + n * 128 + (((q & 7) ^ (n & 7)) << 4);
+          if (n < n16) {
+            *reinterpret_cast<float4*>(hi + off) = make_float4(h[0], h[1], h[2], h[3]);
+            if (SPLIT) *reinterpret_cast<float4*>(hi + off + n16 * 128) = make_float4(l[0], l[1], l[2], l[3]);
+          }
         }
       }
     }
@@ -329,10 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_arrive(&sh.wfull);
   };
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ---- rows to TMEM ----
-    const int r = threadIdx.x;
-    const uint32_t lane_base = tmem + (uint32_t(warp * 32) << 16) + kTmemA;
+    const int r = threadIdx.x & 127, half = 32 * (warp >> 2);
+    const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemA;
     int ci = 0, wrun = 0;
     bool ok = true;
     while (ok && walk.next(&it)) {
@@ -355,10 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float* raw = sRaw + st * (kRaw / 4);
           const uint32_t ta = lane_base + ab * kTmemAStage;
           switch (O.d) {
-            case 1: convert<1, SPLIT>(raw, r, kc, ta); break;
-            case 3: convert<3, SPLIT>(raw, r, kc, ta); break;
-            case 5: convert<5, SPLIT>(raw, r, kc, ta); break;
-            default: convert<7, SPLIT>(raw, r, kc, ta); break;
+            case 1: convert<1, SPLIT>(raw, r, half, kc, ta); break;
+            case 3: convert<3, SPLIT>(raw, r, half, kc, ta); break;
+            case 5: convert<5, SPLIT>(raw, r, half, kc, ta); break;
+            default: convert<7, SPLIT>(raw, r, half, kc, ta); break;
           }
           mbar_arrive(&sh.empty[st]);
           tmem_wait_st();
@@ -367,62 +376,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ---- epilogue ----
-    const int r = threadIdx.x - 128;
-    const uint32_t lane_base = tmem + (uint32_t((warp - 4) * 32) << 16) + kTmemD;
+    const int et = threadIdx.x - 256, r = et & 127, half = 32 * ((warp - 8) >> 2);
+    const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemD;
     int ti = 0, oi = 0, wrun = 0;
     bool ok = true;  // a warp that gave up keeps passing the group's barriers
-    while (walk.next(&it)) {
+    auto node_of = [&](const Item& q) { return half == 0 && r < q.count ? P.perm[q.first + r] : -1; };
+    Item ahead;
+    bool more = walk.next(&ahead);
+    int node = more ? node_of(ahead) : -1;
+    while (more) {
+      it = ahead;
+      const int cur = node;
+      more = walk.next(&ahead);
+      if (more) node = node_of(ahead);  // read a tile ahead: its latency is that of HBM
       const Entry& O = E[it.e];
       const int db = ti & 1;
       float* stage = sOut + (outs == 2 ? oi & 1 : 0) * (kRaw / 4);
-      int node = r < it.count ? P.perm[it.first + r] : -1;
       if (!it.zero && it.run) {
         if (ok && wrun > 0) ok = wait(&sh.wfree, (wrun - 1) & 1, limit, abort, 9);
         if (ok) load_weight(O, it.t);
         ++wrun;
       }
-      if (outs == 1) asm volatile("bar.sync 1, 128;" ::: "memory");  // the last tile has been read
-      sh.node_out[oi & 1][r] = (node >= 0 && node < P.N) ? node : -1;
+      if (outs == 1) asm volatile("bar.sync 1, 256;" ::: "memory");  // the last tile has been read
+      if (half == 0) sh.node_out[oi & 1][r] = (cur >= 0 && cur < P.N) ? cur : -1;
       if (!it.zero) {
         if (ok) ok = wait(&sh.dfull[db], (ti >> 1) & 1, limit, abort, 4);
         if (ok) {
           fence_after_sync();
-          const uint32_t td = lane_base + db * kNT;
+          const uint32_t td = lane_base + db * kTmemDStage;
           switch (O.d) {
-            case 1: lay_out<1>(td, stage, r, O.nw); break;
-            case 3: lay_out<3>(td, stage, r, O.nw); break;
-            case 5: lay_out<5>(td, stage, r, O.nw); break;
-            default: lay_out<7>(td, stage, r, O.nw); break;
+            case 1: lay_out<1, SPLIT>(td, stage, r, half, O.nw); break;
+            case 3: lay_out<3, SPLIT>(td, stage, r, half, O.nw); break;
+            case 5: lay_out<5, SPLIT>(td, stage, r, half, O.nw); break;
+            default: lay_out<7, SPLIT>(td, stage, r, half, O.nw); break;
           }
           fence_before_sync();
           mbar_arrive(&sh.dempty[db]);
         }
         ++ti;
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       if (ok) {
-        const int pitch = node_pitch(O.d);
+        const int pitch = node_pitch(O.d), dim = P.dim_out;
         float* out = P.out + O.off;
         const int* nodes = sh.node_out[oi & 1];
-#pragma unroll 4
-        for (Pieces<VEC> p(it.count, O.nw * O.d, r, 128); p.valid(); p.advance()) {
-          const int n = nodes[p.q];
-          if (n < 0) continue;
-          float* dst = out + int64_t(n) * P.dim_out + p.o * VEC;
-          const float* src = stage + p.q * pitch + p.o * VEC;
-          if constexpr (VEC == 4)
-            *reinterpret_cast<float4*>(dst) = it.zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src);
-          else
-            *dst = it.zero ? 0.f : *src;
+        // four pieces at a time, read before any is stored
+        for (Pieces<VEC> p(it.count, O.nw * O.d, et, 256); p.valid();) {
+          float4 v[4];
+          float* dst[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = p.valid();
+            const int q = in ? p.q : 0, n = nodes[q];
+            const float* src = stage + q * pitch + p.o * VEC;
+            dst[i] = in && n >= 0 ? out + int64_t(n) * dim + p.o * VEC : nullptr;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!it.zero) {
+              if constexpr (VEC == 4)
+                v[i] = *reinterpret_cast<const float4*>(src);
+              else
+                v[i].x = *src;
+            }
+            p.advance();
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (dst[i]) {
+              if constexpr (VEC == 4)
+                *reinterpret_cast<float4*>(dst[i]) = v[i];
+              else
+                *dst[i] = v[i].x;
+            }
         }
       }
       ++oi;
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // ---- node rows to shared memory, several chunks ahead ----
-    const int r = threadIdx.x - 256;
+    const int r = threadIdx.x - 512;
     int ci = 0, ni = 0;
     bool ok = true, more = false;
     auto next_item = [&](Item* q) {  // the next tile with a product
@@ -451,10 +484,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 5)) ok = false;
           if (!ok) break;
           const uint32_t dst = smem_u32(sRaw + st * (kRaw / 4));
-#pragma unroll 4
-          for (Pieces<VEC> p(cur.count, min(kKC, Q.k - k0) * O.d, r, 128); p.valid(); p.advance())
-            copy_async<VEC>(dst + (p.q * pitch + p.o * VEC) * 4,
-                            x + int64_t(nodes[p.q]) * P.dim_src + k0 * O.d + p.o * VEC);
+          for (Pieces<VEC> p(cur.count, min(kKC, Q.k - k0) * O.d, r, 128); p.valid();) {
+            const float* src[4];  // four pieces at a time
+            uint32_t to[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int q = p.valid() ? p.q : 0;
+              src[i] = p.valid() ? x + int64_t(nodes[q]) * P.dim_src + k0 * O.d + p.o * VEC : nullptr;
+              to[i] = dst + (q * pitch + p.o * VEC) * 4;
+              p.advance();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (src[i]) copy_async<VEC>(to[i], src[i]);
+          }
           copies_arrive(&sh.full[st]);
         }
       }
@@ -468,12 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.zero) continue;
       const Entry& O = E[it.e];
       const int db = ti & 1;
-      const uint32_t idesc = idesc_tf32(128, (O.nw + 15) & ~15);
-      const uint32_t td = tmem + kTmemD + db * kNT;
+      const int n16 = (O.nw + 15) & ~15;
+      const uint32_t id1 = idesc_tf32(128, SPLIT ? 2 * n16 : n16), id2 = idesc_tf32(128, n16);
+      const uint32_t td = tmem + kTmemD + db * kTmemDStage;
       if (it.run && !wait(&sh.wfull, wrun & 1, limit, abort, 6)) break;
       if (it.run) ++wrun;
       if (ti >= 2 && !wait(&sh.dempty[db], ((ti >> 1) + 1) & 1, limit, abort, 7)) break;
-      uint32_t acc = 0;
       int wc = 0;
       for (int s = 0; ok && s < O.count; ++s) {
         const int K = S[O.first + s].k;
@@ -486,23 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after_sync();
           if (lane == 0) {
             const uint32_t a = tmem + kTmemA + ab * kTmemAStage;
-            const uint64_t bh = sw128_kmajor(smem_u32(sW + wc * kWChunk)), bl = sw128_kmajor(smem_u32(sW + wc * kWChunk + kWHalf));
-            if (SPLIT) {
-              if (steps == 8) {
+            const uint64_t b = sw128_kmajor(smem_u32(sW + wc * kWChunk));
 #pragma unroll
-                for (int k = 0; k < 8; ++k) issue(td, a, bh, bl, idesc, k, k > 0 ? 1u : acc, true);
-              } else {
-                for (int k = 0; k < steps; ++k) issue(td, a, bh, bl, idesc, k, k > 0 ? 1u : acc, true);
-              }
-              acc = 1;
+            for (int k = 0; k < kKC / 8; ++k) {
+              if (k >= steps) break;
+              // (the descriptor's address field counts 16 bytes: 32 bytes a step)
+              const uint64_t bk = b + uint64_t((k >> 2) * (kWHalf / 16) + (k & 3) * 2);
+              mma_tf32_ta(td, a + 8 * k, bk, id1, wc > 0 || k > 0);
+              if (SPLIT) mma_tf32_ta(td + n16, a + kKC + 8 * k, bk, id2, 1);
             }
-            if (steps == 8) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) issue(td, a, bh, bl, idesc, k, k > 0 ? 1u : acc, false);
-            } else {
-              for (int k = 0; k < steps; ++k) issue(td, a, bh, bl, idesc, k, k > 0 ? 1u : acc, false);
-            }
-            acc = 1;
             mma_commit(&sh.aempty[ab]);
           }
           __syncwarp();
@@ -523,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 20) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
