@@ -382,12 +382,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
         if (!ok) continue;
         const uint32_t dst = smem_u32(sRaw + st * stage_bytes);
+        auto rows = [&](const float* src, int dim, int len, uint32_t to0) {
+          const int n = len / VEC;
+          const RowShare w(n, r, kCopy);
+          for (int o = w.at; o < n; o += w.pieces) {
+            uint32_t to = to0 + (w.row * len + o * VEC) * 4;
 #pragma unroll 4
-        for (Pieces<VEC> p(cnt, lx, r, kCopy); p.valid(); p.advance())
-          copy_async<VEC>(dst + p.i * (4 * VEC), x + int64_t(nodes[p.q]) * P.dim_x + p.o * VEC);
-#pragma unroll 4
-        for (Pieces<VEC> p(cnt, lg, r, kCopy); p.valid(); p.advance())
-          copy_async<VEC>(dst + g_offset + p.i * (4 * VEC), g + int64_t(nodes[p.q]) * P.dim_g + p.o * VEC);
+            for (int k = w.row; k < cnt; k += w.rows, to += w.rows * len * 4)
+              copy_async<VEC>(to, src + o * VEC + int64_t(nodes[k]) * dim);
+          }
+        };
+        rows(x, P.dim_x, lx, dst);
+        rows(g, P.dim_g, lg, dst + g_offset);
         copies_arrive(&sh.full[st]);
       }
     }

@@ -29,7 +29,7 @@
 // One persistent CTA per SM takes an equal share of the (block, columns) x types x
 // tiles list, in order, so that its weight changes rarely; the group sizes are read
 // from the device.  Warps 0-7 convert (two per 32 rows, 32 channels each), 8-15 run the
-// epilogue (two per 32 rows, 32 columns each), 16-19 copy, 20 issues the MMAs: with one
+// epilogue (two per 32 rows, 32 columns each), 16-20 copy, 21 issues the MMAs: with one
 // warpgroup for each role their latencies, not the issue slots (36 % busy), bounded
 // the tile.  (Bulk copies of a node's piece were tried in place of the copy threads: about
 // 60 cycles of issue a copy, 2.5 times the time at 64 scalars a node.)
@@ -61,7 +61,7 @@ constexpr int kWChunk = 2 * kWHalf;
 constexpr int kRaw = 32928;                   // a raw chunk or an output tile (see node_pitch)
 constexpr int kMaxStages = 4;
 constexpr int kSMemMax = 227 * 1024;
-constexpr int kThreads = 672;
+constexpr int kThreads = 704, kCopy = 160;     // copy threads: whole rows of 16, 48, 80, 112 pieces fill them
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemA = 0, kTmemAStage = 128, kTmemD = 256, kTmemDStage = 128;  // A: 2 x (hi 64 | lo 64), D: 2 x (D1 | D2)
 
@@ -99,7 +99,7 @@ struct Shared {
   uint64_t afull[2], aempty[2], dfull[2], dempty[2], wfull, wfree, fin;
   uint32_t tmem;
   int abort;
-  int total[4];                    // tiles of all groups for d = 1, 3, 5, 7
+  int total[4];                    // tiles of all types for d = 1, 3, 5, 7
   int node_in[2][128], node_out[2][128];
 };
 
@@ -108,13 +108,13 @@ __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, uint64_t limi
 }
 
 // ---- the CTA's share of the work -------------------------------------------------
-// Entries in order, in each the tiles of groups 0..T; CTA b owns the tiles whose cost
+// Entries in order, in each the tiles of the types; CTA b owns the tiles whose cost
 // begins in its share.  Every warp walks the same list.
 struct Item {
   int e, t, first, count;
   bool run;       // the first tile with this weight
   bool run_last;  // the last tile of this CTA with this weight
-  bool zero;      // no product: a group without a type, or a block without a source
+  bool zero;      // no product: a block without a source
 };
 
 struct Walk {
@@ -152,9 +152,9 @@ struct Walk {
         unit = tile_of(E[e].d);
         empty = E[e].count == 0;
         int j;
-        seek_unit(offs, T + 1, unit, a, &t, &j);
-        end = t <= T ? offs[t + 1] : 0;
-        at = t <= T ? offs[t] + j * unit : 0;
+        seek_unit(offs, T, unit, a, &t, &j);
+        end = t < T ? offs[t + 1] : 0;
+        at = t < T ? offs[t] + j * unit : 0;
         fresh = true;
         return true;
       }
@@ -163,7 +163,7 @@ struct Walk {
   __device__ bool next(Item* it) {
     if (left == 0 && !next_entry()) return false;
     while (at >= end) {
-      if (t >= T) return false;
+      if (t + 1 >= T) return false;
       ++t, fresh = true;
       at = offs[t], end = offs[t + 1];
     }
@@ -171,7 +171,7 @@ struct Walk {
     it->first = at;
     it->count = min(unit, end - at);
     it->run = fresh;
-    it->zero = empty || t >= T;
+    it->zero = empty;
     fresh = false;
     at += unit, --left;
     it->run_last = left == 0 || at >= end;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   load_offsets(offs, P.offsets, P.T, P.N);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&sh.full[s], 128);
+      mbar_init(&sh.full[s], kCopy);
       mbar_init(&sh.empty[s], 256);
     }
     for (int i = 0; i < 2; ++i) {
@@ -288,13 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 20) tmem_alloc(&sh.tmem, kTmemCols);
+  if (warp == 21) tmem_alloc(&sh.tmem, kTmemCols);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = sh.tmem;
   if (warp < 4) {
-    const int n = count_units(offs, P.T + 1, tile_of(2 * warp + 1));
+    const int n = count_units(offs, P.T, tile_of(2 * warp + 1));
     if (lane == 0) sh.total[warp] = n;
   }
   __syncthreads();
@@ -386,6 +386,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item ahead;
     bool more = walk.next(&ahead);
     int node = more ? node_of(ahead) : -1;
+    // this CTA's share of the nodes without a type: zero rows, a warp each
+    {
+      const int b = offs[P.T], nz = max(int(P.N) - b, 0);
+      const int z0 = b + int(share_begin(nz, blockIdx.x, gridDim.x)), z1 = b + int(share_begin(nz, blockIdx.x + 1, gridDim.x));
+      for (int i = z0 + (warp - 8); i < z1; i += 8) {
+        const int n = P.perm[i];
+        if (n < 0 || n >= P.N) continue;
+        float* dst = P.out + int64_t(n) * P.dim_out;
+        for (int c = lane * VEC; c < P.dim_out; c += 32 * VEC) {
+          if constexpr (VEC == 4)
+            *reinterpret_cast<float4*>(dst + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+          else
+            dst[c] = 0.f;
+        }
+      }
+    }
     while (more) {
       it = ahead;
       const int cur = node;
@@ -422,38 +438,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pitch = node_pitch(O.d), dim = P.dim_out;
         float* out = P.out + O.off;
         const int* nodes = sh.node_out[oi & 1];
-        // four pieces at a time, read before any is stored
-        for (Pieces<VEC> p(it.count, O.nw * O.d, et, 256); p.valid();) {
-          float4 v[4];
-          float* dst[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool in = p.valid();
-            const int q = in ? p.q : 0, n = nodes[q];
-            const float* src = stage + q * pitch + p.o * VEC;
-            dst[i] = in && n >= 0 ? out + int64_t(n) * dim + p.o * VEC : nullptr;
-            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!it.zero) {
-              if constexpr (VEC == 4)
-                v[i] = *reinterpret_cast<const float4*>(src);
-              else
-                v[i].x = *src;
+        const int n = O.nw * O.d / VEC;
+        const RowShare w(n, et, 256);
+        for (int o = w.at; o < n; o += w.pieces) {
+          const float* src = stage + w.row * pitch + o * VEC;
+#pragma unroll 4
+          for (int q = w.row; q < it.count; q += w.rows, src += w.rows * pitch) {
+            const int node = nodes[q];
+            float* dst = out + int64_t(node) * dim + o * VEC;
+            if constexpr (VEC == 4) {
+              const float4 v = it.zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src);
+              if (node >= 0) *reinterpret_cast<float4*>(dst) = v;
+            } else {
+              const float v = it.zero ? 0.f : *src;
+              if (node >= 0) *dst = v;
             }
-            p.advance();
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (dst[i]) {
-              if constexpr (VEC == 4)
-                *reinterpret_cast<float4*>(dst[i]) = v[i];
-              else
-                *dst[i] = v[i].x;
-            }
         }
       }
       ++oi;
     }
-  } else if (warp < 20) {
+  } else if (warp < 21) {
     // ---- node rows to shared memory, several chunks ahead ----
     const int r = threadIdx.x - 512;
     int ci = 0, ni = 0;
@@ -472,10 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Entry& O = E[cur.e];
       int* nodes = sh.node_in[ni & 1];
       ++ni;
-      nodes[r] = (node >= 0 && node < P.N) ? node : 0;  // (a wrong node's row is not stored)
+      if (r < 128) nodes[r] = (node >= 0 && node < P.N) ? node : 0;  // (a wrong node's row is not stored)
       more = next_item(&it);
       if (more) node = node_of(it);  // read while this tile is copied
-      asm volatile("bar.sync 2, 128;" ::: "memory");
+      asm volatile("bar.sync 2, 160;" ::: "memory");
       for (int s = 0; ok && s < O.count; ++s) {
         const LinSource& Q = S[O.first + s];
         const float* x = P.x[Q.pair] + Q.off;
@@ -484,19 +489,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 5)) ok = false;
           if (!ok) break;
           const uint32_t dst = smem_u32(sRaw + st * (kRaw / 4));
-          for (Pieces<VEC> p(cur.count, min(kKC, Q.k - k0) * O.d, r, 128); p.valid();) {
-            const float* src[4];  // four pieces at a time
-            uint32_t to[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int q = p.valid() ? p.q : 0;
-              src[i] = p.valid() ? x + int64_t(nodes[q]) * P.dim_src + k0 * O.d + p.o * VEC : nullptr;
-              to[i] = dst + (q * pitch + p.o * VEC) * 4;
-              p.advance();
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (src[i]) copy_async<VEC>(to[i], src[i]);
+          const int n = min(kKC, Q.k - k0) * O.d / VEC;
+          const RowShare w(n, r, kCopy);
+          for (int o = w.at; o < n; o += w.pieces) {
+            const float* src = x + k0 * O.d + o * VEC;
+            uint32_t to = dst + (w.row * pitch + o * VEC) * 4;
+#pragma unroll 4
+            for (int q = w.row; q < cur.count; q += w.rows, to += w.rows * pitch * 4)
+              copy_async<VEC>(to, src + int64_t(nodes[q]) * P.dim_src);
           }
           copies_arrive(&sh.full[st]);
         }
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 20) {
+  if (warp == 21) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -625,7 +625,7 @@ cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStr
       P.e[P.n_entries++] = {O.d, cost, O.off + c0 * O.d, std::min(kNT, O.n - c0), c0, O.first, O.count, 0};
       P.coef[O.d >> 1] += cost;
     }
-    tiles += (R.N / tile_of(O.d) + std::min<int64_t>(R.T + 1, R.N)) * col_tiles(O.n);
+    tiles += (R.N / tile_of(O.d) + std::min<int64_t>(R.T, R.N)) * col_tiles(O.n);
   }
   const bool v = vec4(R);
   auto* k = split ? (v ? k_linear_tc<true, 4> : k_linear_tc<true, 1>) : (v ? k_linear_tc<false, 4> : k_linear_tc<false, 1>);

@@ -66,24 +66,19 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Pieces of VEC floats of `rows` rows of `len` floats, dealt out to `threads`
-// threads in order: piece i is row q, offset o of that row.
-template <int VEC>
-struct Pieces {
-  int q, o, n, dq, dr, total, i, step;
-  __device__ __forceinline__ Pieces(int rows, int len, int thread, int threads) {
-    n = len / VEC;
-    total = rows * n;
-    i = thread, step = threads;
-    q = thread / n, o = thread - q * n;
-    dq = threads / n, dr = threads - dq * n;
-  }
-  __device__ __forceinline__ bool valid() const { return i < total; }
-  __device__ __forceinline__ void advance() {
-    i += step;
-    q += dq;
-    o += dr;
-    if (o >= n) o -= n, ++q;
+// How `threads` threads share rows of `n` pieces: as many whole rows at a time as
+// fit (or, for longer rows, the pieces of one row in turn); a thread keeps its place
+// in the row, so that a step costs an addition and not a division.
+struct RowShare {
+  int row, at;       // this thread's first row and piece
+  int rows, pieces;  // rows, or pieces of one row, that a step covers
+  __device__ __forceinline__ RowShare(int n, int thread, int threads) {
+    const int r = threads / n;
+    rows = r > 0 ? r : 1;
+    pieces = r > 0 ? n : threads;
+    row = r > 0 ? thread / n : 0;
+    at = r > 0 ? thread - row * n : thread;
+    if (row >= rows) at = n;  // a thread left over
   }
 };
 
