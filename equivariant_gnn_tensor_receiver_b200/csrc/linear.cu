@@ -290,8 +290,9 @@ void fill_rows(const tpconv_linear* p, bool transposed, int pairs, LinRows* R) {
 }
 
 cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph, cudaStream_t st) {
-  if (p->gemm != TPCONV_GEMM_SIMT && linear_tc_supported(R)) {
-    ph.note(1);
+  const int tc = p->gemm != TPCONV_GEMM_SIMT ? linear_tc_launches(R) : 0;
+  if (tc > 0) {
+    ph.note(tc);
     return linear_tc_rows(R, p->gemm == TPCONV_GEMM_FP32, device_wait_limit(), st);
   }
   int colt = 1, dmax = 1;

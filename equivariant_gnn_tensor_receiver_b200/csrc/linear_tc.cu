@@ -28,11 +28,14 @@
 //
 // One persistent CTA per SM takes an equal share of the (block, columns) x types x
 // tiles list, in order, so that its weight changes rarely; the group sizes are read
-// from the device.  Warps 0-7 convert (two per 32 rows, 32 channels each), 8-15 run the
-// epilogue (two per 32 rows, 32 columns each), 16-20 copy, 21 issues the MMAs: with one
-// warpgroup for each role their latencies, not the issue slots (36 % busy), bounded
-// the tile.  (Bulk copies of a node's piece were tried in place of the copy threads: about
-// 60 cycles of issue a copy, 2.5 times the time at 64 scalars a node.)
+// from the device.  What bounds a tile is the latency of its steps, not the issue
+// slots, so two pipelines take every second tile each, with buffers and barriers of
+// their own, and share the weight: warps 0-3 and 4-7 convert, 8-11 and 12-15 run the
+// epilogue, 21 and 22 issue the MMAs; 16-20 copy for both.
+// (Bulk copies of a node's piece were tried in place of the copy threads: about 60
+// cycles of issue a copy, 2.5 times the time at 64 scalars a node.  Both warpgroups of
+// a role on one tile: 340 us against 306 at 262144 nodes of 64x0e+64x1o+64x2e.)
+// A sum over more than 160 channels runs in several passes that add to the output.
 // Every wait is bounded by the call's limit; on expiry the kernel records it, stops
 // issuing, waits (bounded) for its own copies and MMAs, frees TMEM and returns.
 #include <cuda_runtime.h>
@@ -53,15 +56,14 @@ __device__ int g_linear_error;  // first code recorded by an expired wait (0 = n
 
 constexpr int kSMs = 148;
 constexpr int kNT = 64, kKC = 64;             // columns of a tile, channels of a chunk
-constexpr int kMaxChunks = kLinTcChunks;      // chunks of a resident weight
-// one chunk of a weight: 32 channels behind 32 channels, each the rows of up to 64 output
-// channels' hi and behind them their lo, 128 bytes a row (K-major, 128-byte swizzle)
+// 32 channels of a weight: the rows of up to 64 output channels' hi and behind them their
+// lo, 128 bytes a row (K-major, 128-byte swizzle)
 constexpr int kWHalf = 2 * kNT * 32 * 4;
-constexpr int kWChunk = 2 * kWHalf;
+constexpr int kMaxHalves = 5;                 // of a resident weight: 160 channels
 constexpr int kRaw = 32928;                   // a raw chunk or an output tile (see node_pitch)
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 2;                 // raw chunks of a pipeline
 constexpr int kSMemMax = 227 * 1024;
-constexpr int kThreads = 704, kCopy = 160;     // copy threads: whole rows of 16, 48, 80, 112 pieces fill them
+constexpr int kThreads = 736, kCopy = 160;     // copy threads: whole rows of 16, 48, 80, 112 pieces fill them
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemA = 0, kTmemAStage = 128, kTmemD = 256, kTmemDStage = 128;  // A: 2 x (hi 64 | lo 64), D: 2 x (D1 | D2)
 
@@ -72,7 +74,8 @@ static_assert(tile_of(1) * node_pitch(1) * 4 <= kRaw && tile_of(3) * node_pitch(
                   tile_of(5) * node_pitch(5) * 4 <= kRaw && tile_of(7) * node_pitch(7) * 4 <= kRaw,
               "a tile fits its buffer");
 
-constexpr int chunks_of(int k) { return (k + kKC - 1) / kKC; }
+__host__ __device__ constexpr int chunks_of(int k) { return (k + kKC - 1) / kKC; }
+__host__ __device__ constexpr int halves_of(int k) { return (k + 31) / 32; }
 constexpr int col_tiles(int n) { return (n + kNT - 1) / kNT; }
 
 // (output block, 64 columns)
@@ -89,13 +92,14 @@ struct Params {
   const float *x[2], *w[2];
   float* out;
   const int *perm, *offsets;
-  int coef[4];  // cost of a tile of d = 1, 3, 5, 7, summed over the entries
+  int coef[4];     // cost of a tile of d = 1, 3, 5, 7, summed over the entries
+  int accumulate;  // add to the output (and leave the rows without a type alone)
   Entry e[kLinTcEntries];
   LinSource s[kLinSources];
 };
 
 struct Shared {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[2][kMaxStages], empty[2][kMaxStages];
   uint64_t afull[2], aempty[2], dfull[2], dempty[2], wfull, wfree, fin;
   uint32_t tmem;
   int abort;
@@ -179,55 +183,42 @@ struct Walk {
   }
 };
 
-// a node's row m, channels k0 .. k0+15 of the raw chunk (zeros at and behind kc)
-template <int D, bool WHOLE>
-__device__ __forceinline__ void read_row16(const float* row, int k0, int kc, float (&v)[16]) {
+// 16 channels of a node's row m: raw -> hi (and lo) in TMEM, zeros at and behind n
+template <int D, bool SPLIT, bool WHOLE>
+__device__ __forceinline__ void convert16(const float* row, int n, uint32_t ta) {
+  float v[16], h[16];
   if constexpr (D == 1) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 q = *reinterpret_cast<const float4*>(row + k0 + 4 * i);
+      const float4 q = *reinterpret_cast<const float4*>(row + 4 * i);
       v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-    }
-    if constexpr (!WHOLE) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = k0 + i < kc ? v[i] : 0.f;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = (WHOLE || k0 + i < kc) ? row[(k0 + i) * D] : 0.f;
+    for (int i = 0; i < 16; ++i) v[i] = (WHOLE || i < n) ? row[i * D] : 0.f;
   }
-}
-template <int D, bool SPLIT, bool WHOLE>
-__device__ __forceinline__ void convert16(const float* row, int k0, int kc, uint32_t ta) {
-  float v[16], h[16];
-  read_row16<D, WHOLE>(row, k0, kc, v);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) tf32_split<SPLIT>(v[i], h[i], v[i]);
-  tmem_st16(ta + k0, h);
-  if (SPLIT) tmem_st16(ta + kKC + k0, v);
+  for (int i = 0; i < 16; ++i) tf32_split<SPLIT>((D > 1 || WHOLE || i < n) ? v[i] : 0.f, h[i], v[i]);
+  tmem_st16(ta, h);
+  if (SPLIT) tmem_st16(ta + kKC, v);
 }
-// 32 channels of one chunk of the thread's row: raw -> hi (and lo) in TMEM
+// one chunk of the thread's row
 template <int D, bool SPLIT>
-__device__ __forceinline__ void convert(const float* raw, int r, int first, int kc, uint32_t ta) {
+__device__ __forceinline__ void convert(const float* raw, int r, int kc, uint32_t ta) {
   constexpr int ROWS = tile_of(D) * D;
   const int rr = r < ROWS ? r : ROWS - 1;
   const float* row = raw + (rr / D) * node_pitch(D) + rr % D;
-#pragma unroll
-  for (int i = 0; i < 32; i += 16) {
-    if (first + i + 16 <= kc)
-      convert16<D, SPLIT, true>(row, first + i, kc, ta);
-    else if (first + i < kc)
-      convert16<D, SPLIT, false>(row, first + i, kc, ta);
-  }
+  int k0 = 0;
+#pragma unroll 1
+  for (; k0 + 16 <= kc; k0 += 16, row += 16 * D) convert16<D, SPLIT, true>(row, 16, ta + k0);
+  if (k0 < kc) convert16<D, SPLIT, false>(row, kc - k0, ta + k0);
 }
 template <int D, bool SPLIT>
-__device__ __forceinline__ void lay_out(uint32_t td, float* stage, int r, int first, int nw) {
+__device__ __forceinline__ void lay_out(uint32_t td, float* stage, int r, int nw) {
   constexpr int ROWS = tile_of(D) * D;
   float* row = stage + (r / D) * node_pitch(D) + r % D;
-#pragma unroll
-  for (int i = 0; i < 32; i += 16) {
-    const int c = first + i;
-    if (c >= nw) break;
+#pragma unroll 1
+  for (int c = 0; c < nw; c += 16, row += 16 * D) {
     float v[16];
     tmem_ld16(td + c, v);
     if (SPLIT) {
@@ -240,10 +231,10 @@ __device__ __forceinline__ void lay_out(uint32_t td, float* stage, int r, int fi
       if constexpr (D == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4*>(row + c + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          *reinterpret_cast<float4*>(row + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) row[(c + i) * D] = v[i];
+        for (int i = 0; i < 16; ++i) row[i * D] = v[i];
       }
     }
   }
@@ -251,14 +242,14 @@ __device__ __forceinline__ void lay_out(uint32_t td, float* stage, int r, int fi
 
 template <bool SPLIT, int VEC>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_linear_tc(const __grid_constant__ Params P, int chunks, int stages, int outs, uint64_t limit) {
+    k_linear_tc(const __grid_constant__ Params P, int halves, int stages, uint64_t limit) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* sW = base;
-  float* sRaw = reinterpret_cast<float*>(base + chunks * kWChunk);
-  float* sOut = sRaw + stages * (kRaw / 4);
-  LinSource* S = reinterpret_cast<LinSource*>(sOut + outs * (kRaw / 4));
+  float* sRaw = reinterpret_cast<float*>(base + halves * kWHalf);
+  float* sOut = sRaw + 2 * stages * (kRaw / 4);
+  LinSource* S = reinterpret_cast<LinSource*>(sOut + 2 * (kRaw / 4));
   Entry* E = reinterpret_cast<Entry*>(S + P.n_src);
   int* offs = reinterpret_cast<int*>(E + P.n_entries);
   __shared__ Shared sh;
@@ -272,19 +263,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     reinterpret_cast<int*>(E)[i] = reinterpret_cast<const int*>(P.e)[i];
   load_offsets(offs, P.offsets, P.T, P.N);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&sh.full[s], kCopy);
-      mbar_init(&sh.empty[s], 256);
-    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.afull[i], 256);
+      for (int s = 0; s < kMaxStages; ++s) {
+        mbar_init(&sh.full[i][s], kCopy);
+        mbar_init(&sh.empty[i][s], 128);
+      }
+      mbar_init(&sh.afull[i], 128);
       mbar_init(&sh.aempty[i], 1);
       mbar_init(&sh.dfull[i], 1);
-      mbar_init(&sh.dempty[i], 256);
+      mbar_init(&sh.dempty[i], 128);
     }
     mbar_init(&sh.wfull, 512);
-    mbar_init(&sh.wfree, 1);
-    mbar_init(&sh.fin, 1);
+    mbar_init(&sh.wfree, 2);
+    mbar_init(&sh.fin, 2);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -304,12 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the weight of a run, by the converter and epilogue threads: thread (n, q0) takes four channels at a time
   auto load_weight = [&](const Entry& O, int t) {
     const int n = threadIdx.x & 63, n16 = (O.nw + 15) & ~15;
-    int c = 0;
+    unsigned char* hi = sW;
     for (int s = 0; s < O.count; ++s) {
       const LinSource& Q = S[O.first + s];
       const float* w = P.w[Q.pair] + int64_t(t) * P.wnumel + Q.woff + int64_t(O.c0 + n) * Q.rw;
-      for (int k0 = 0; k0 < Q.k; k0 += kKC, ++c) {
-        unsigned char* hi = sW + c * kWChunk;
+      for (int k0 = 0; k0 < Q.k; k0 += kKC) {
         const int kc = min(kKC, Q.k - k0);
         float v[2][4];
 #pragma unroll
@@ -327,11 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int f = 0; f < 4; ++f) tf32_split<SPLIT>(v[i][f], h[f], l[f]);
           // (the lo rows begin at a multiple of 16: the same swizzle)
           const int off = (q >> 3) * kWHalf + n * 128 + (((q & 7) ^ (n & 7)) << 4);
-          if (n < n16) {
+          if (n < n16 && q < 8 * halves_of(kc)) {
             *reinterpret_cast<float4*>(hi + off) = make_float4(h[0], h[1], h[2], h[3]);
             if (SPLIT) *reinterpret_cast<float4*>(hi + off + n16 * 128) = make_float4(l[0], l[1], l[2], l[3]);
           }
         }
+        hi += halves_of(kc) * kWHalf;
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -339,10 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 8) {
-    // ---- rows to TMEM ----
-    const int r = threadIdx.x & 127, half = 32 * (warp >> 2);
-    const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemA;
-    int ci = 0, wrun = 0;
+    // ---- rows to TMEM: tiles of the set's parity ----
+    const int r = threadIdx.x & 127, set = warp >> 2;
+    const uint32_t ta = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemA + set * kTmemAStage;
+    int ci = 0, ti = 0, wrun = 0;  // the set's chunks, all tiles, all runs
     bool ok = true;
     while (ok && walk.next(&it)) {
       if (it.zero) continue;
@@ -353,41 +344,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_weight(O, it.t);
         ++wrun;
       }
+      if ((ti++ & 1) != set) continue;
       for (int s = 0; ok && s < O.count; ++s) {
         const int K = S[O.first + s].k;
         for (int k0 = 0; k0 < K; k0 += kKC, ++ci) {
-          const int st = ci % stages, ab = ci & 1, kc = min(kKC, K - k0);
-          if (ci >= 2 && !wait(&sh.aempty[ab], ((ci >> 1) + 1) & 1, limit, abort, 2)) ok = false;
-          if (ok && !wait(&sh.full[st], (ci / stages) & 1, limit, abort, 3)) ok = false;
+          const int st = ci % stages, kc = min(kKC, K - k0);
+          if (ci >= 1 && !wait(&sh.aempty[set], (ci - 1) & 1, limit, abort, 2)) ok = false;
+          if (ok && !wait(&sh.full[set][st], (ci / stages) & 1, limit, abort, 3)) ok = false;
           if (!ok) break;
           fence_after_sync();
-          const float* raw = sRaw + st * (kRaw / 4);
-          const uint32_t ta = lane_base + ab * kTmemAStage;
+          const float* raw = sRaw + (set * stages + st) * (kRaw / 4);
           switch (O.d) {
-            case 1: convert<1, SPLIT>(raw, r, half, kc, ta); break;
-            case 3: convert<3, SPLIT>(raw, r, half, kc, ta); break;
-            case 5: convert<5, SPLIT>(raw, r, half, kc, ta); break;
-            default: convert<7, SPLIT>(raw, r, half, kc, ta); break;
+            case 1: convert<1, SPLIT>(raw, r, kc, ta); break;
+            case 3: convert<3, SPLIT>(raw, r, kc, ta); break;
+            case 5: convert<5, SPLIT>(raw, r, kc, ta); break;
+            default: convert<7, SPLIT>(raw, r, kc, ta); break;
           }
-          mbar_arrive(&sh.empty[st]);
+          mbar_arrive(&sh.empty[set][st]);
           tmem_wait_st();
           fence_before_sync();
-          mbar_arrive(&sh.afull[ab]);
+          mbar_arrive(&sh.afull[set]);
         }
       }
     }
   } else if (warp < 16) {
-    // ---- epilogue ----
-    const int et = threadIdx.x - 256, r = et & 127, half = 32 * ((warp - 8) >> 2);
-    const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemD;
-    int ti = 0, oi = 0, wrun = 0;
-    bool ok = true;  // a warp that gave up keeps passing the group's barriers
-    auto node_of = [&](const Item& q) { return half == 0 && r < q.count ? P.perm[q.first + r] : -1; };
-    Item ahead;
-    bool more = walk.next(&ahead);
-    int node = more ? node_of(ahead) : -1;
+    // ---- epilogue: tiles of the set's parity ----
+    const int r = threadIdx.x & 127, set = (warp - 8) >> 2;
+    const uint32_t td = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemD + set * kTmemDStage;
+    float* stage = sOut + set * (kRaw / 4);
+    int* nodes = sh.node_out[set];
+    int ti = 0, di = 0, wrun = 0;  // tiles, tiles with a product
+    bool ok = true;  // a warp that gave up keeps passing the set's barriers
+    auto bar = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory"); };
+    // the next tile of the set; on the way, its part of the weights of new runs
+    auto next_item = [&](int* d) {
+      for (;;) {
+        if (!walk.next(&it)) return false;
+        *d = di;
+        if (!it.zero) ++di;
+        if (!it.zero && it.run) {
+          if (ok && wrun > 0) ok = wait(&sh.wfree, (wrun - 1) & 1, limit, abort, 9);
+          if (ok) load_weight(E[it.e], it.t);
+          ++wrun;
+        }
+        // a tile with a product goes to the set of its accumulator
+        if (it.zero ? (ti++ & 1) == set : (*d & 1) == set) return true;
+      }
+    };
     // this CTA's share of the nodes without a type: zero rows, a warp each
-    {
+    if (!P.accumulate) {
       const int b = offs[P.T], nz = max(int(P.N) - b, 0);
       const int z0 = b + int(share_begin(nz, blockIdx.x, gridDim.x)), z1 = b + int(share_begin(nz, blockIdx.x + 1, gridDim.x));
       for (int i = z0 + (warp - 8); i < z1; i += 8) {
@@ -402,66 +407,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    while (more) {
-      it = ahead;
-      const int cur = node;
-      more = walk.next(&ahead);
-      if (more) node = node_of(ahead);  // read a tile ahead: its latency is that of HBM
+    int d;
+    while (next_item(&d)) {
       const Entry& O = E[it.e];
-      const int db = ti & 1;
-      float* stage = sOut + (outs == 2 ? oi & 1 : 0) * (kRaw / 4);
-      if (!it.zero && it.run) {
-        if (ok && wrun > 0) ok = wait(&sh.wfree, (wrun - 1) & 1, limit, abort, 9);
-        if (ok) load_weight(O, it.t);
-        ++wrun;
-      }
-      if (outs == 1) asm volatile("bar.sync 1, 256;" ::: "memory");  // the last tile has been read
-      if (half == 0) sh.node_out[oi & 1][r] = (cur >= 0 && cur < P.N) ? cur : -1;
+      const int node = r < it.count ? P.perm[it.first + r] : -1;
+      bar();  // the set's last tile has been read
       if (!it.zero) {
-        if (ok) ok = wait(&sh.dfull[db], (ti >> 1) & 1, limit, abort, 4);
+        if (ok) ok = wait(&sh.dfull[set], (d >> 1) & 1, limit, abort, 4);
         if (ok) {
           fence_after_sync();
-          const uint32_t td = lane_base + db * kTmemDStage;
           switch (O.d) {
-            case 1: lay_out<1, SPLIT>(td, stage, r, half, O.nw); break;
-            case 3: lay_out<3, SPLIT>(td, stage, r, half, O.nw); break;
-            case 5: lay_out<5, SPLIT>(td, stage, r, half, O.nw); break;
-            default: lay_out<7, SPLIT>(td, stage, r, half, O.nw); break;
+            case 1: lay_out<1, SPLIT>(td, stage, r, O.nw); break;
+            case 3: lay_out<3, SPLIT>(td, stage, r, O.nw); break;
+            case 5: lay_out<5, SPLIT>(td, stage, r, O.nw); break;
+            default: lay_out<7, SPLIT>(td, stage, r, O.nw); break;
           }
           fence_before_sync();
-          mbar_arrive(&sh.dempty[db]);
+          mbar_arrive(&sh.dempty[set]);
         }
-        ++ti;
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      nodes[r] = (node >= 0 && node < P.N) ? node : -1;
+      bar();
       if (ok) {
-        const int pitch = node_pitch(O.d), dim = P.dim_out;
-        float* out = P.out + O.off;
-        const int* nodes = sh.node_out[oi & 1];
-        const int n = O.nw * O.d / VEC;
-        const RowShare w(n, et, 256);
+        const int pitch = node_pitch(O.d), dim = P.dim_out, n = O.nw * O.d / VEC;
+        const RowShare w(n, r, 128);
         for (int o = w.at; o < n; o += w.pieces) {
           const float* src = stage + w.row * pitch + o * VEC;
+          float* out = P.out + O.off + o * VEC;
 #pragma unroll 4
           for (int q = w.row; q < it.count; q += w.rows, src += w.rows * pitch) {
-            const int node = nodes[q];
-            float* dst = out + int64_t(node) * dim + o * VEC;
+            const int m = nodes[q];
+            float* dst = out + int64_t(m) * dim;
             if constexpr (VEC == 4) {
-              const float4 v = it.zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src);
-              if (node >= 0) *reinterpret_cast<float4*>(dst) = v;
+              float4 v = it.zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src);
+              if (m >= 0) {
+                if (P.accumulate) {
+                  const float4 u = *reinterpret_cast<const float4*>(dst);
+                  v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+                }
+                *reinterpret_cast<float4*>(dst) = v;
+              }
             } else {
               const float v = it.zero ? 0.f : *src;
-              if (node >= 0) *dst = v;
+              if (m >= 0) *dst = P.accumulate ? *dst + v : v;
             }
           }
         }
       }
-      ++oi;
     }
   } else if (warp < 21) {
     // ---- node rows to shared memory, several chunks ahead ----
     const int r = threadIdx.x - 512;
-    int ci = 0, ni = 0;
+    int ci[2] = {0, 0}, ni = 0;  // chunks of each pipeline, tiles
     bool ok = true, more = false;
     auto next_item = [&](Item* q) {  // the next tile with a product
       bool m;
@@ -475,20 +472,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (more) {  // (a warp that gave up keeps passing the group's barriers)
       const Item cur = it;
       const Entry& O = E[cur.e];
-      int* nodes = sh.node_in[ni & 1];
+      const int set = ni & 1;
+      int* nodes = sh.node_in[set];
       ++ni;
       if (r < 128) nodes[r] = (node >= 0 && node < P.N) ? node : 0;  // (a wrong node's row is not stored)
       more = next_item(&it);
       if (more) node = node_of(it);  // read while this tile is copied
-      asm volatile("bar.sync 2, 160;" ::: "memory");
+      asm volatile("bar.sync 3, 160;" ::: "memory");
       for (int s = 0; ok && s < O.count; ++s) {
         const LinSource& Q = S[O.first + s];
         const float* x = P.x[Q.pair] + Q.off;
-        for (int k0 = 0; k0 < Q.k; k0 += kKC, ++ci) {
-          const int st = ci % stages, pitch = node_pitch(O.d);
-          if (ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 5)) ok = false;
+        for (int k0 = 0; k0 < Q.k; k0 += kKC) {
+          const int c = set ? ci[1]++ : ci[0]++, st = c % stages, pitch = node_pitch(O.d);
+          if (c >= stages && !wait(&sh.empty[set][st], ((c / stages) + 1) & 1, limit, abort, 5)) ok = false;
           if (!ok) break;
-          const uint32_t dst = smem_u32(sRaw + st * (kRaw / 4));
+          const uint32_t dst = smem_u32(sRaw + (set * stages + st) * (kRaw / 4));
           const int n = min(kKC, Q.k - k0) * O.d / VEC;
           const RowShare w(n, r, kCopy);
           for (int o = w.at; o < n; o += w.pieces) {
@@ -498,55 +496,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = w.row; q < cur.count; q += w.rows, to += w.rows * pitch * 4)
               copy_async<VEC>(to, src + int64_t(nodes[q]) * P.dim_src);
           }
-          copies_arrive(&sh.full[st]);
+          copies_arrive(&sh.full[set][st]);
         }
       }
     }
     copies_wait_all();  // no copy may be in flight when the CTA ends
   } else {
-    // ---- MMAs ----
+    // ---- MMAs: tiles of the warp's parity ----
+    const int set = warp - 21;
     int ci = 0, ti = 0, wrun = 0;
     bool ok = true;
     while (ok && walk.next(&it)) {
       if (it.zero) continue;
       const Entry& O = E[it.e];
-      const int db = ti & 1;
-      const int n16 = (O.nw + 15) & ~15;
-      const uint32_t id1 = idesc_tf32(128, SPLIT ? 2 * n16 : n16), id2 = idesc_tf32(128, n16);
-      const uint32_t td = tmem + kTmemD + db * kTmemDStage;
-      if (it.run && !wait(&sh.wfull, wrun & 1, limit, abort, 6)) break;
-      if (it.run) ++wrun;
-      if (ti >= 2 && !wait(&sh.dempty[db], ((ti >> 1) + 1) & 1, limit, abort, 7)) break;
-      int wc = 0;
-      for (int s = 0; ok && s < O.count; ++s) {
-        const int K = S[O.first + s].k;
-        for (int k0 = 0; k0 < K; k0 += kKC, ++ci, ++wc) {
-          const int ab = ci & 1, steps = (min(kKC, K - k0) + 7) / 8;
-          if (!wait(&sh.afull[ab], (ci >> 1) & 1, limit, abort, 8)) {
-            ok = false;
-            break;
-          }
-          fence_after_sync();
-          if (lane == 0) {
-            const uint32_t a = tmem + kTmemA + ab * kTmemAStage;
-            const uint64_t b = sw128_kmajor(smem_u32(sW + wc * kWChunk));
-#pragma unroll
-            for (int k = 0; k < kKC / 8; ++k) {
-              if (k >= steps) break;
-              // (the descriptor's address field counts 16 bytes: 32 bytes a step)
-              const uint64_t bk = b + uint64_t((k >> 2) * (kWHalf / 16) + (k & 3) * 2);
-              mma_tf32_ta(td, a + 8 * k, bk, id1, wc > 0 || k > 0);
-              if (SPLIT) mma_tf32_ta(td + n16, a + kKC + 8 * k, bk, id2, 1);
+      // every run in turn, with or without a tile: an arrival at wfree must not run ahead of its phase
+      if (it.run && !wait(&sh.wfull, wrun++ & 1, limit, abort, 6)) break;
+      if ((ti & 1) == set) {
+        const int n16 = (O.nw + 15) & ~15;
+        const uint32_t id1 = idesc_tf32(128, SPLIT ? 2 * n16 : n16), id2 = idesc_tf32(128, n16);
+        const uint32_t td = tmem + kTmemD + set * kTmemDStage;
+        if (ti >= 2 && !wait(&sh.dempty[set], ((ti >> 1) + 1) & 1, limit, abort, 7)) break;
+        uint32_t wo = 0;  // the chunk's place in the weight
+        for (int s = 0; ok && s < O.count; ++s) {
+          const int K = S[O.first + s].k;
+          for (int k0 = 0; k0 < K; k0 += kKC, ++ci) {
+            const int kc = min(kKC, K - k0), steps = (kc + 7) / 8;
+            if (!wait(&sh.afull[set], ci & 1, limit, abort, 8)) {
+              ok = false;
+              break;
             }
-            mma_commit(&sh.aempty[ab]);
+            fence_after_sync();
+            if (lane == 0) {
+              const uint32_t a = tmem + kTmemA + set * kTmemAStage;
+              const uint64_t b = sw128_kmajor(smem_u32(sW) + wo);
+#pragma unroll
+              for (int k = 0; k < kKC / 8; ++k) {
+                if (k >= steps) break;
+                // (the descriptor's address field counts 16 bytes: 32 bytes a step)
+                const uint64_t bk = b + uint64_t((k >> 2) * (kWHalf / 16) + (k & 3) * 2);
+                mma_tf32_ta(td, a + 8 * k, bk, id1, wo > 0 || k > 0);
+                if (SPLIT) mma_tf32_ta(td + n16, a + kKC + 8 * k, bk, id2, 1);
+              }
+              mma_commit(&sh.aempty[set]);
+            }
+            __syncwarp();
+            wo += halves_of(kc) * kWHalf;
           }
-          __syncwarp();
         }
+        if (ok && lane == 0) mma_commit(&sh.dfull[set]);
       }
-      if (ok && lane == 0) {
-        mma_commit(&sh.dfull[db]);
-        if (it.run_last) mma_commit(&sh.wfree);
-      }
+      // the weight is free once both warps' products with it have completed
+      if (ok && it.run_last && lane == 0) mma_commit(&sh.wfree);
       __syncwarp();
       ++ti;
     }
@@ -564,29 +564,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// the shape of a call: chunks of its widest weight, shared memory behind it
-struct Shape {
-  int chunks, entries, stages, outs, bytes;
-};
-Shape shape_of(const LinRows& R) {
-  Shape h{0, 0, 0, 0, 0};
-  for (int b = 0; b < R.n_out; ++b) {
-    const LinOut& O = R.o[b];
-    int c = 0;
-    for (int s = 0; s < O.count; ++s) c += chunks_of(R.s[O.first + s].k);
-    h.chunks = std::max(h.chunks, c);
-    h.entries += col_tiles(O.n);
-  }
-  const int lists = R.n_src * int(sizeof(LinSource)) + h.entries * int(sizeof(Entry)) + (R.T + 2) * 4;
-  // the weight, then as many raw stages (two to four) and output buffers (one or two) as fit
-  const int fixed = 1024 + h.chunks * kWChunk + lists;
-  const int room = (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / kRaw;
-  h.outs = room >= 5 ? 2 : 1;
-  h.stages = std::min(kMaxStages, room - h.outs);
-  h.bytes = fixed + (h.stages + h.outs) * kRaw;
-  return h;
-}
-
 bool vec4(const LinRows& R) {
   const auto bad = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; };
   if (R.dim_src % 4 || R.dim_out % 4 || bad(R.out)) return false;
@@ -601,38 +578,91 @@ bool vec4(const LinRows& R) {
   return true;
 }
 
+// the passes of an output block: its sources' chunks in order, as many as a weight holds
+int passes_of(const LinRows& R, const LinOut& O) {
+  int pass = 0, halves = 0;
+  for (int s = 0; s < O.count; ++s) {
+    const int K = R.s[O.first + s].k;
+    for (int c = 0; c < chunks_of(K); ++c) {
+      const int h = halves_of(std::min(kKC, K - c * kKC));
+      if (halves + h > kMaxHalves) ++pass, halves = 0;
+      halves += h;
+    }
+  }
+  return pass + 1;
+}
+
 }  // namespace
 
-bool linear_tc_supported(const LinRows& R) {
-  const Shape h = shape_of(R);
-  return h.chunks <= kMaxChunks && h.entries <= kLinTcEntries && h.stages >= 2;
+int linear_tc_launches(const LinRows& R) {
+  int entries = 0, passes = 1;
+  for (int b = 0; b < R.n_out; ++b) {
+    entries += col_tiles(R.o[b].n);
+    passes = std::max(passes, passes_of(R, R.o[b]));
+  }
+  return entries <= kLinTcEntries ? passes : 0;
 }
 
 cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStream_t st) {
-  const Shape h = shape_of(R);
-  Params P;
-  std::memset(&P, 0, sizeof(P));
-  P.n_src = R.n_src, P.T = R.T, P.dim_src = R.dim_src, P.dim_out = R.dim_out, P.N = R.N, P.wnumel = R.wnumel;
-  for (int i = 0; i < 2; ++i) P.x[i] = R.x[i], P.w[i] = R.w[i];
-  P.out = R.out, P.perm = R.perm, P.offsets = R.offsets;
-  std::copy(R.s, R.s + R.n_src, P.s);
-  int64_t tiles = 0;
-  for (int b = 0; b < R.n_out; ++b) {
-    const LinOut& O = R.o[b];
-    int cost = 1;
-    for (int s = 0; s < O.count; ++s) cost += chunks_of(R.s[O.first + s].k);
-    for (int c0 = 0; c0 < O.n; c0 += kNT) {
-      P.e[P.n_entries++] = {O.d, cost, O.off + c0 * O.d, std::min(kNT, O.n - c0), c0, O.first, O.count, 0};
-      P.coef[O.d >> 1] += cost;
-    }
-    tiles += (R.N / tile_of(O.d) + std::min<int64_t>(R.T, R.N)) * col_tiles(O.n);
-  }
   const bool v = vec4(R);
-  auto* k = split ? (v ? k_linear_tc<true, 4> : k_linear_tc<true, 1>) : (v ? k_linear_tc<false, 4> : k_linear_tc<false, 1>);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, h.bytes);
-  if (e) return e;
-  k<<<unsigned(std::min<int64_t>(kSMs, tiles)), kThreads, h.bytes, st>>>(P, h.chunks, h.stages, h.outs, limit);
-  return cudaGetLastError();
+  auto* kernel = split ? (v ? k_linear_tc<true, 4> : k_linear_tc<true, 1>)
+                       : (v ? k_linear_tc<false, 4> : k_linear_tc<false, 1>);
+  const int passes = linear_tc_launches(R);
+  for (int pass = 0; pass < passes; ++pass) {
+    Params P;
+    std::memset(&P, 0, sizeof(P));
+    P.T = R.T, P.dim_src = R.dim_src, P.dim_out = R.dim_out, P.N = R.N, P.wnumel = R.wnumel;
+    for (int i = 0; i < 2; ++i) P.x[i] = R.x[i], P.w[i] = R.w[i];
+    P.out = R.out, P.perm = R.perm, P.offsets = R.offsets, P.accumulate = pass > 0;
+    int64_t tiles = 0;
+    int most = 0;
+    for (int b = 0; b < R.n_out; ++b) {
+      const LinOut& O = R.o[b];
+      // the pass's chunks of the block's sources, neighbours together
+      const int first = P.n_src;
+      int chunks = 0, halves = 0, at = 0, cur = 0;
+      for (int s = 0; s < O.count; ++s) {
+        const LinSource& S = R.s[O.first + s];
+        int lo = -1, hi = -1;
+        for (int c = 0; c < chunks_of(S.k); ++c) {
+          const int h = halves_of(std::min(kKC, S.k - c * kKC));
+          if (cur + h > kMaxHalves) ++at, cur = 0;
+          cur += h;
+          if (at != pass) continue;
+          if (lo < 0) lo = c;
+          hi = c + 1;
+          ++chunks;
+          halves += h;
+        }
+        if (lo < 0) continue;
+        LinSource& q = P.s[P.n_src++];
+        q = S;
+        q.off += lo * kKC * O.d, q.woff += int64_t(lo) * kKC * S.rk;
+        q.k = std::min(S.k, hi * kKC) - lo * kKC;
+      }
+      if (pass > 0 && chunks == 0) continue;
+      most = std::max(most, halves);
+      for (int c0 = 0; c0 < O.n; c0 += kNT) {
+        P.e[P.n_entries++] = {O.d, chunks + 1, O.off + c0 * O.d, std::min(kNT, O.n - c0), c0, first, P.n_src - first, 0};
+        P.coef[O.d >> 1] += chunks + 1;
+      }
+      tiles += (R.N / tile_of(O.d) + std::min<int64_t>(R.T, R.N)) * col_tiles(O.n);
+    }
+    // shared memory: the weight, and for each pipeline an output tile and as many raw chunks (one or two) as fit
+    const int fixed = 1024 + most * kWHalf + 2 * kRaw + P.n_src * int(sizeof(LinSource)) +
+                      P.n_entries * int(sizeof(Entry)) + (P.T + 2) * 4;
+    static_assert(1024 + kMaxHalves * kWHalf + 4 * kRaw + kLinSources * int(sizeof(LinSource)) +
+                          kLinTcEntries * int(sizeof(Entry)) + (TPCONV_MAX_TYPES + 2) * 4 + int(sizeof(Shared)) + 64 <=
+                      kSMemMax,
+                  "a raw chunk always fits");
+    const int stages = std::min(kMaxStages, (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / (2 * kRaw));
+    const int bytes = fixed + 2 * stages * kRaw;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e) return e;
+    kernel<<<unsigned(std::min<int64_t>(kSMs, tiles)), kThreads, bytes, st>>>(P, most, stages, limit);
+    if ((e = cudaGetLastError())) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t linear_tc_read_error(int* code) {

@@ -5,11 +5,10 @@
 
 namespace tpc {
 
-constexpr int kLinTcChunks = 4;    // 64-channel chunks of a resident weight: up to 256 source channels
 constexpr int kLinTcEntries = 48;  // (output block, 64 columns) pairs of a call
 
-// whether the weights of every (block, columns, type) stay resident
-bool linear_tc_supported(const LinRows& R);
+// kernels that the product launches; 0: it has too many (output block, 64 columns) pairs
+int linear_tc_launches(const LinRows& R);
 // the row product; split = 3xTF32, else one TF32 pass
 cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStream_t st);
 // first code recorded by an expired wait since the last read (0 = none); clears it

@@ -188,7 +188,9 @@ LINEARS = [
     ("128x0e+128x1o+128x2e+128x3o", "32x0e+32x1o+32x2e", 400, 5), ("4x1o", "4x1e", 20, 2), ("8x0e", "8x0e+4x2e", 50, 3),
     ("16x3o+12x2e", "20x3o+8x2e", 77, 256), ("64x0e", "64x0e", 3000, 2), ("260x0e+100x1o", "130x0e+260x1o", 150, 3),
     ("32x0e+16x1o", "32x0e+16x1o", 0, 3), ("64x1o", "64x1o", 1, 5), ("96x0e+64x0e", "72x0e", 333, 4),
-    ("200x0e+4x0e", "64x0e", 140, 2)]
+    ("200x0e+4x0e", "64x0e", 140, 2), ("64x0e+64x1o+64x2e", "64x0e+64x1o+64x2e", 4096, 10),
+    ("32x0e+32x1o", "64x0e+32x1o", 2500, 60), ("128x0e+128x1o+128x2e", "96x0e+130x1o+8x2e", 1500, 9),
+    ("20x0e+20x0e+20x0e+20x0e+20x0e+300x1o", "16x0e+8x1o", 900, 31)]
 
 
 def linear_inputs(irr, n, n_types, seed, padded=0.15):
