@@ -281,6 +281,7 @@ class LinearPlan:
                                           GEMM[gemm]))
         self.handle = h
         self.irreps_in, self.irreps_out, self.n_types, self.gemm = irreps_in, irreps_out, int(n_types), gemm
+        self._bytes = {}
         a = [ctypes.c_int() for _ in range(4)]
         w = ctypes.c_size_t()
         _check("tpconv_linear_info", lib().tpconv_linear_info(h, *[ctypes.byref(v) for v in a], ctypes.byref(w)))
@@ -293,6 +294,13 @@ class LinearPlan:
                                                                   ctypes.byref(w)))
             l, ci, co, ib, ob = (x.value for x in v)
             self.paths.append(dict(l=l, c_in=ci, c_out=co, in_block=ib, out_block=ob, weight_offset=w.value))
+
+    def workspace_bytes(self, op, N):
+        """Workspace of a call, kept for the last node count of each operation."""
+        c = self._bytes.get(op)
+        if c is None or c[0] != N:
+            c = self._bytes[op] = (N, tpconv_linear_workspace_size(self, op, N))
+        return c[1]
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -309,9 +317,17 @@ class NormPlan:
         _check("tpconv_norm_create", lib().tpconv_norm_create(ctypes.byref(h), irreps.encode(), float(eps)))
         self.handle = h
         self.irreps, self.eps = irreps, float(eps)
+        self._bytes = {}
         a = [ctypes.c_int() for _ in range(4)]
         _check("tpconv_norm_info", lib().tpconv_norm_info(h, *[ctypes.byref(v) for v in a]))
         self.n_blocks, self.dim, self.weight_numel, self.bias_numel = (v.value for v in a)
+
+    def workspace_bytes(self, op, N):
+        """Workspace of a call, kept for the last node count of each operation."""
+        c = self._bytes.get(op)
+        if c is None or c[0] != N:
+            c = self._bytes[op] = (N, tpconv_norm_workspace_size(self, op, N))
+        return c[1]
 
     def __del__(self):
         h = getattr(self, "handle", None)

@@ -3,15 +3,16 @@
 //   perm    = node ids by key, ascending inside a key (key = type, or n_types for
 //             any other value), offsets[t] = number of nodes with a key below t.
 //
-// The N ids are cut into tiles of consecutive nodes.  A tile's warps own
-// consecutive pieces of it; the lanes of a warp that hold the same key find each
-// other (match) and their ranks follow from the lane order, so a node's place is
+// The N ids are cut into tiles of consecutive nodes, worked on 4096 at a time.  A
+// tile's warps own consecutive pieces of 128; the lanes of a warp that hold the same key
+// find each other (match) and their ranks follow from the lane order, so a node's place is
 //   offsets[key] + nodes of that key in earlier tiles + in earlier warps + rank:
 // no atomics decide an order, and the result is the stable one.
 // Up to kSingle nodes run as one tile in one launch (the call's latency is all);
-// more run as two launches: histograms per tile, then every tile adds up the
-// histograms before its own (a table of tiles x (n_types + 1) ints that stays in
-// L2) and scatters.  Work: 4 bytes read twice and 4 written per node.
+// more run as two launches: histograms per tile (shared-memory atomics: a count has no
+// order), then every tile adds up the histograms before its own (a table of
+// (n_types + 1) x tiles ints that stays in L2) and scatters.  Work: 4 bytes read twice
+// and 4 written per node.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -24,50 +25,38 @@ namespace {
 
 constexpr int kWarps = 32;                 // of a CTA
 constexpr int kKeys = TPCONV_MAX_TYPES + 1;
-constexpr int kSingle = 8192;              // nodes handled by one CTA alone
-constexpr int kTile = 4096;                // nodes of a tile otherwise (at least)
+constexpr int kSteps = 4;                  // nodes of a lane at a time
+constexpr int kSub = 32 * kWarps * kSteps; // nodes of a CTA at a time
+constexpr int kSingle = 2 * kSub;          // nodes handled by one CTA alone
 constexpr int kMaxTiles = 592;
 
-__device__ __forceinline__ int key_of(const int* type, int64_t i, int T) {
-  const int t = type[i];
-  return (t >= 0 && t < T) ? t : T;
-}
-
-// nodes of a tile for N nodes: a multiple of 32 * kWarps
-inline int64_t tile_nodes(int64_t N) {
-  int64_t per = (N + kMaxTiles - 1) / kMaxTiles;
-  per = std::max<int64_t>(per, kTile);
-  return (per + 32 * kWarps - 1) / (32 * kWarps) * (32 * kWarps);
-}
-
-// cnt[warp][key] = nodes of that key in the warp's piece [w0, w1) of the tile
-__device__ __forceinline__ void count_piece(const int* type, int64_t w0, int64_t w1, int T, int* mine) {
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = w0; i < w1; i += 32) {
-    const int64_t n = i + lane;
-    const bool in = n < w1;
-    const int k = in ? key_of(type, n, T) : -1;
-    const unsigned peers = __match_any_sync(0xffffffffu, k);
-    if (in && lane == __ffs(peers) - 1) mine[k] += __popc(peers);
-    __syncwarp();
+// the keys of the lane's nodes first, first + 32, ...; -1 behind n
+__device__ __forceinline__ void load_keys(const int* type, int64_t first, int64_t n, int T, int (&key)[kSteps]) {
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int64_t p = first + 32 * i;
+    const int t = p < n ? type[p] : 0;
+    key[i] = p < n ? ((t >= 0 && t < T) ? t : T) : -1;
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) k_group_count(int64_t N, int64_t tile, int T,
+__global__ void __launch_bounds__(kWarps * 32) k_group_count(int64_t N, int64_t tile, int T, int tiles,
                                                              const int* __restrict__ type, int* __restrict__ hist) {
-  extern __shared__ int cnt[];  // [kWarps][T + 1]
-  const int K = T + 1, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < kWarps * K; i += blockDim.x) cnt[i] = 0;
+  __shared__ int cnt[4][kKeys];  // (copies: less contention on a common type)
+  const int K = T + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < 4 * kKeys; i += blockDim.x) cnt[i / kKeys][i % kKeys] = 0;
   __syncthreads();
-  const int64_t t0 = blockIdx.x * tile, piece = tile / kWarps;
-  const int64_t w0 = min(t0 + warp * piece, N), w1 = min(t0 + (warp + 1) * piece, N);
-  count_piece(type, w0, w1, T, cnt + warp * K);
-  __syncthreads();
-  for (int k = threadIdx.x; k < K; k += blockDim.x) {
-    int s = 0;
-    for (int w = 0; w < kWarps; ++w) s += cnt[w * K + k];
-    hist[int64_t(blockIdx.x) * K + k] = s;
+  const int64_t t0 = blockIdx.x * tile, t1 = min(t0 + tile, N);
+  for (int64_t s = t0; s < t1; s += kSub) {
+    int key[kSteps];
+    load_keys(type, s + warp * (32 * kSteps) + lane, t1, T, key);
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      if (key[i] >= 0) atomicAdd(&cnt[warp & 3][key[i]], 1);
   }
+  __syncthreads();
+  for (int k = threadIdx.x; k < K; k += blockDim.x)
+    hist[int64_t(k) * tiles + blockIdx.x] = cnt[0][k] + cnt[1][k] + cnt[2][k] + cnt[3][k];
 }
 
 // place of every node of one tile.  tiles == 1: the tile is everything and no
@@ -76,40 +65,38 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_place(int64_t N, int64_t 
                                                              const int* __restrict__ type,
                                                              const int* __restrict__ hist, int* __restrict__ perm,
                                                              int* __restrict__ offsets) {
-  extern __shared__ int cnt[];  // [kWarps][K] counts, then cursors; [K] before, [K] totals
+  extern __shared__ int cnt[];  // [kWarps][K] counts, then cursors; [K] next place, [K] totals
   const int K = T + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* before = cnt + kWarps * K;
-  int* total = before + K;
-  for (int i = threadIdx.x; i < (kWarps + 2) * K; i += blockDim.x) cnt[i] = 0;
-  __syncthreads();
-  const int64_t t0 = blockIdx.x * tile, piece = tile / kWarps;
-  const int64_t w0 = min(t0 + warp * piece, N), w1 = min(t0 + (warp + 1) * piece, N);
-  count_piece(type, w0, w1, T, cnt + warp * K);
+  int* place = cnt + kWarps * K;
+  int* total = place + K;
+  const int64_t t0 = blockIdx.x * tile, t1 = min(t0 + tile, N);
   if (tiles > 1) {
     // key by key, the warps' lanes add up the tiles' histograms
     for (int k = warp; k < K; k += kWarps) {
       int b = 0, s = 0;
+#pragma unroll 4
       for (int t = lane; t < tiles; t += 32) {
-        const int h = hist[int64_t(t) * K + k];
+        const int h = hist[int64_t(k) * tiles + t];
         s += h;
-        if (t < int(blockIdx.x)) b += h;
+        b += t < int(blockIdx.x) ? h : 0;
       }
       s = __reduce_add_sync(0xffffffffu, s);
       b = __reduce_add_sync(0xffffffffu, b);
-      if (lane == 0) before[k] = b, total[k] = s;
+      if (lane == 0) place[k] = b, total[k] = s;
+    }
+  } else {
+    for (int k = threadIdx.x; k < K; k += blockDim.x) place[k] = total[k] = 0;
+    __syncthreads();
+    for (int64_t s = t0; s < t1; s += kSub) {
+      int key[kSteps];
+      load_keys(type, s + warp * (32 * kSteps) + lane, t1, T, key);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        if (key[i] >= 0) atomicAdd(&total[key[i]], 1);
     }
   }
   __syncthreads();
-  if (tiles == 1) {
-    for (int k = threadIdx.x; k < K; k += blockDim.x) {
-      int s = 0;
-      for (int w = 0; w < kWarps; ++w) s += cnt[w * K + k];
-      total[k] = s;
-    }
-    __syncthreads();
-  }
-  // exclusive scan of the totals over the keys (one warp), then the cursors
-  if (warp == 0) {
+  if (warp == 0) {  // exclusive scan of the totals over the keys
     int carry = 0;
     for (int k0 = 0; k0 < K; k0 += 32) {
       const int k = k0 + lane;
@@ -123,34 +110,49 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_place(int64_t N, int64_t 
       if (k < K) {
         const int first = carry + s - v;
         if (blockIdx.x == 0) offsets[k] = first;  // offsets[T] = first node of no group
-        before[k] += first;
+        place[k] += first;
       }
       carry += __shfl_sync(0xffffffffu, s, 31);
     }
   }
-  __syncthreads();
-  for (int k = threadIdx.x; k < K; k += blockDim.x) {
-    int s = before[k];
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = cnt[w * K + k];
-      cnt[w * K + k] = s;
-      s += c;
+  int* mine = cnt + warp * K;
+  for (int64_t s = t0; s < t1; s += kSub) {
+    const int64_t first = s + warp * (32 * kSteps) + lane;
+    int key[kSteps], rank[kSteps];
+    load_keys(type, first, t1, T, key);
+    for (int k = lane; k < K; k += 32) mine[k] = 0;
+    __syncwarp();
+    // ranks inside the warp's piece
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const unsigned peers = __match_any_sync(0xffffffffu, key[i]);
+      const int before = __popc(peers & ((1u << lane) - 1));
+      rank[i] = key[i] >= 0 ? mine[key[i]] + before : 0;
+      __syncwarp();
+      if (key[i] >= 0 && before == 0) mine[key[i]] += __popc(peers);
+      __syncwarp();
     }
-  }
-  __syncthreads();
-  int* cur = cnt + warp * K;
-  for (int64_t i = w0; i < w1; i += 32) {
-    const int64_t n = i + lane;
-    const bool in = n < w1;
-    const int k = in ? key_of(type, n, T) : -1;
-    const unsigned peers = __match_any_sync(0xffffffffu, k);
-    const int rank = __popc(peers & ((1u << lane) - 1));
-    if (in) perm[cur[k] + rank] = int(n);
-    __syncwarp();
-    if (in && rank == 0) cur[k] += __popc(peers);
-    __syncwarp();
+    __syncthreads();
+    for (int k = threadIdx.x; k < K; k += blockDim.x) {
+      int at = place[k];
+#pragma unroll 8
+      for (int w = 0; w < kWarps; ++w) {
+        const int c = cnt[w * K + k];
+        cnt[w * K + k] = at;
+        at += c;
+      }
+      place[k] = at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      if (key[i] >= 0) perm[mine[key[i]] + rank[i]] = int(first + 32 * i);
+    __syncthreads();
   }
 }
+
+// nodes of a tile for N nodes: a multiple of kSub
+int64_t tile_nodes(int64_t N) { return ((N + kMaxTiles - 1) / kMaxTiles + kSub - 1) / kSub * kSub; }
 
 size_t place_smem(int T) { return size_t(kWarps + 2) * (T + 1) * 4; }
 static_assert((kWarps + 2) * kKeys * 4 <= 48 * 1024, "the counters fit the default shared memory");
@@ -196,7 +198,7 @@ int tpconv_group_nodes(int64_t N, int n_types, const int32_t* type, int32_t* per
     const int64_t tile = tile_nodes(N);
     const int tiles = int((N + tile - 1) / tile);
     int* hist = static_cast<int*>(workspace);
-    k_group_count<<<tiles, kWarps * 32, size_t(kWarps) * (n_types + 1) * 4, st>>>(N, tile, n_types, type, hist);
+    k_group_count<<<tiles, kWarps * 32, 0, st>>>(N, tile, n_types, tiles, type, hist);
     if (cudaGetLastError()) return TPCONV_ERR_CUDA;
     k_group_place<<<tiles, kWarps * 32, place_smem(n_types), st>>>(N, tile, n_types, tiles, type, hist, perm, offsets);
     ph.note(2);

@@ -9,34 +9,43 @@ and workspace are allocated for that stream.
 
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _lib as L
 
-
-def _need(name, t, shape, device, dtype=torch.float32):
-    if t is None:
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensor must be contiguous")
+_F32, _I32 = torch.float32, torch.int32
 
 
-def _cuda_device(name, t):
+def _refuse(name, t, shape, dev, dtype):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: tensor must be on a CUDA device")
-    return t.device
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name}: tensor must be contiguous")
+
+
+def _ptr(name, t, shape, dev, optional=False):
+    """Device address of a checked fp32 tensor (None stands for a null pointer where that is allowed)."""
+    if t is None and optional:
+        return None
+    if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not _F32 or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(name, t, shape, dev, _F32)
+    return t.data_ptr()
+
+
+def _device_of(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor must be on a CUDA device")
+    return t.get_device()
 
 
 def _wanted(want, names):
@@ -45,32 +54,76 @@ def _wanted(want, names):
     return want
 
 
-@contextlib.contextmanager
-def _on(device, stream, *tensors):
-    """The device current and, with an explicit stream, that stream too: what is allocated inside belongs to it
+class _Here:
+    """No context to enter: the device is current and the call runs on its current stream."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *_):
+        pass
+
+
+class _There:
+    """The device current and, with an explicit stream, that stream too: what is allocated inside belongs to it,
     and the inputs are not reused before its work on them is done."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
-            for t in tensors:
+
+    def __init__(self, dev, stream, tensors):
+        self.dev, self.stream, self.tensors = torch.cuda.device(dev), stream, tensors
+
+    def __enter__(self):
+        self.dev.__enter__()
+        if self.stream is not None:
+            self.outer = torch.cuda.stream(self.stream)
+            self.outer.__enter__()
+
+    def __exit__(self, *e):
+        if self.stream is not None:
+            self.outer.__exit__(*e)
+            for t in self.tensors:
                 if t is not None and t.numel():
-                    t.record_stream(stream)
+                    t.record_stream(self.stream)
+        self.dev.__exit__(*e)
 
 
-def _new(wanted, shape, device):
-    return torch.empty(shape, dtype=torch.float32, device=device) if wanted else None
+_HERE = _Here()
 
 
-def _ws_for(ws, nbytes, device):
-    """The caller's workspace, checked, or a fresh one."""
+def _on(dev, stream, *tensors):
+    if stream is None and dev == torch.cuda.current_device():
+        return _HERE
+    return _There(dev, stream, tensors)
+
+
+def _raw_stream(dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _new(x, wanted, *shape):
+    """A new tensor beside x and its address, or two Nones."""
+    if not wanted:
+        return None, None
+    t = x.new_empty(shape)
+    return t, t.data_ptr()
+
+
+def _workspace(ws, nbytes, x):
+    """(tensor to keep, address, bytes): the caller's workspace or a fresh one."""
     if ws is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if _cuda_device("ws", ws) != device:
-        raise ValueError(f"ws: expected a tensor on {device}, got {ws.device}")
-    return ws
+        if not nbytes:
+            return None, None, 0
+        ws = x.new_empty(nbytes, dtype=torch.uint8)
+    elif _device_of("ws", ws) != x.get_device():
+        raise ValueError(f"ws: expected a tensor on {x.device}, got {ws.device}")
+    elif not ws.is_contiguous():
+        raise ValueError("ws: tensor must be contiguous")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _run(name, *args):
+    st = getattr(L.lib(), name)(*args)
+    if st:
+        raise L.TPConvError(name, st)
 
 
 class NodeGroups:
@@ -79,131 +132,140 @@ class NodeGroups:
     ``offsets`` [n_types + 1] where each type begins.  ``types`` is an int32 (or int64) vector on the device."""
 
     def __init__(self, types, n_types, stream=None):
-        dev = _cuda_device("types", types)
+        dev = _device_of("types", types)
         if types.dim() != 1 or types.dtype not in (torch.int32, torch.int64):
             raise ValueError("types: expected a vector of int32 or int64")
         n_types = int(n_types)
         if not 1 <= n_types <= L.MAX_TYPES:
             raise ValueError(f"n_types: expected 1..{L.MAX_TYPES}, got {n_types}")
-        self.N, self.n_types, self.device = types.numel(), n_types, dev
+        self.N, self.n_types, self.device, self._dev = types.numel(), n_types, types.device, dev
         with _on(dev, stream, types):
             if types.dtype == torch.int64:  # no wrap-around of far values into a type
-                types = torch.where((types >= 0) & (types < n_types), types, -1).to(torch.int32)
+                types = torch.where((types >= 0) & (types < n_types), types, -1).to(_I32)
             t = types.contiguous()
-            self.perm = torch.empty(self.N, dtype=torch.int32, device=dev)
-            self.offsets = torch.empty(n_types + 1, dtype=torch.int32, device=dev)
-            ws = torch.empty(L.tpconv_group_workspace_size(self.N, n_types), dtype=torch.uint8, device=dev)
-            L.tpconv_group_nodes(self.N, n_types, t, self.perm, self.offsets, ws, stream)
+            self.perm = t.new_empty(self.N)
+            self.offsets = t.new_empty(n_types + 1)
+            _ws, wp, wn = _workspace(None, L.tpconv_group_workspace_size(self.N, n_types), t)
+            _run("tpconv_group_nodes", self.N, n_types, t.data_ptr(), self.perm.data_ptr(), self.offsets.data_ptr(),
+                 wp, wn, _raw_stream(dev, stream))
+        self._perm, self._offsets = self.perm.data_ptr(), self.offsets.data_ptr()
 
 
 # ---- typed linear map ---------------------------------------------------------------------------------
 
 
-def _linear_args(plan, groups, **t):
+def _groups(plan, groups):
     if not isinstance(groups, NodeGroups):
         raise TypeError("groups: expected NodeGroups")
     if groups.n_types != plan.n_types:
         raise ValueError(f"groups: {groups.n_types} types, the plan has {plan.n_types}")
-    shapes = {"x": (groups.N, plan.dim_in), "g": (groups.N, plan.dim_out), "weight": (plan.n_types, plan.weight_numel)}
-    for k, v in t.items():
-        base = k[3:] if k.startswith("gg_") else ("g" if k == "out" else k)
-        if v is None and not k.startswith("gg_") and k != "out":
-            raise TypeError(f"{k}: expected a tensor")
-        _need(k, v, shapes[base], groups.device)
-    return groups.N, groups.device
+    N = groups.N
+    return N, groups._dev, (N, plan.dim_in), (N, plan.dim_out), (plan.n_types, plan.weight_numel)
 
 
 def linear_forward(plan, groups, x, weight, out=None, ws=None, stream=None):
     """out[N, dim_out]: every node's features times the weight of its type; rows of no group are zero."""
-    N, dev = _linear_args(plan, groups, x=x, weight=weight, out=out)
+    N, dev, rin, rout, w = _groups(plan, groups)
+    px, pw = _ptr("x", x, rin, dev), _ptr("weight", weight, w, dev)
     with _on(dev, stream, x, weight, groups.perm, groups.offsets):
         if out is None:
-            out = _new(True, (N, plan.dim_out), dev)
-        ws = _ws_for(ws, L.tpconv_linear_workspace_size(plan, L.OP_FORWARD, N), dev)
-        L.tpconv_linear_forward(plan, N, groups.perm, groups.offsets, x, weight, out, ws, stream)
+            out, po = _new(x, True, *rout)
+        else:
+            po = _ptr("out", out, rout, dev)
+        _ws, wp, wn = _workspace(ws, plan.workspace_bytes(L.OP_FORWARD, N), x)
+        _run("tpconv_linear_forward", plan.handle, N, groups._perm, groups._offsets, px, pw, po, wp, wn,
+             _raw_stream(dev, stream))
     return out
 
 
 def linear_backward(plan, groups, x, weight, g, want=("dx", "dweight"), ws=None, stream=None):
     """{"dx": [N, dim_in], "dweight": [n_types, weight_numel]} for the cotangent g of the output."""
-    N, dev = _linear_args(plan, groups, x=x, weight=weight, g=g)
+    N, dev, rin, rout, w = _groups(plan, groups)
+    px, pw, pg = _ptr("x", x, rin, dev), _ptr("weight", weight, w, dev), _ptr("g", g, rout, dev)
     _wanted(want, ("dx", "dweight"))
     with _on(dev, stream, x, weight, g, groups.perm, groups.offsets):
-        outs = {"dx": _new("dx" in want, (N, plan.dim_in), dev),
-                "dweight": _new("dweight" in want, (plan.n_types, plan.weight_numel), dev)}
-        ws = _ws_for(ws, L.tpconv_linear_workspace_size(plan, L.OP_BACKWARD, N), dev)
-        L.tpconv_linear_backward(plan, N, groups.perm, groups.offsets, x, weight, g, outs["dx"], outs["dweight"], ws,
-                                 stream)
-    return {k: v for k, v in outs.items() if v is not None}
+        dx, pdx = _new(x, "dx" in want, *rin)
+        dw, pdw = _new(x, "dweight" in want, *w)
+        _ws, wp, wn = _workspace(ws, plan.workspace_bytes(L.OP_BACKWARD, N), x)
+        _run("tpconv_linear_backward", plan.handle, N, groups._perm, groups._offsets, px, pw, pg, pdx, pdw, wp, wn,
+             _raw_stream(dev, stream))
+    return {k: v for k, v in (("dx", dx), ("dweight", dw)) if v is not None}
 
 
 def linear_double_backward(plan, groups, x, weight, g, gg_x=None, gg_weight=None, want=("d_g", "d_x", "d_weight"),
                            ws=None, stream=None):
     """Gradients of <gg_x, dx> + <gg_weight, dweight> by g, x and weight (a cotangent None = zero)."""
-    N, dev = _linear_args(plan, groups, x=x, weight=weight, g=g, gg_x=gg_x, gg_weight=gg_weight)
+    N, dev, rin, rout, w = _groups(plan, groups)
+    px, pw, pg = _ptr("x", x, rin, dev), _ptr("weight", weight, w, dev), _ptr("g", g, rout, dev)
+    pa, pal = _ptr("gg_x", gg_x, rin, dev, True), _ptr("gg_weight", gg_weight, w, dev, True)
     _wanted(want, ("d_g", "d_x", "d_weight"))
     with _on(dev, stream, x, weight, g, gg_x, gg_weight, groups.perm, groups.offsets):
-        outs = {"d_g": _new("d_g" in want, (N, plan.dim_out), dev), "d_x": _new("d_x" in want, (N, plan.dim_in), dev),
-                "d_weight": _new("d_weight" in want, (plan.n_types, plan.weight_numel), dev)}
-        ws = _ws_for(ws, L.tpconv_linear_workspace_size(plan, L.OP_DOUBLE_BACKWARD, N), dev)
-        L.tpconv_linear_double_backward(plan, N, groups.perm, groups.offsets, x, weight, g, gg_x, gg_weight,
-                                        outs["d_g"], outs["d_x"], outs["d_weight"], ws, stream)
-    return {k: v for k, v in outs.items() if v is not None}
+        d_g, pdg = _new(x, "d_g" in want, *rout)
+        d_x, pdx = _new(x, "d_x" in want, *rin)
+        d_w, pdw = _new(x, "d_weight" in want, *w)
+        _ws, wp, wn = _workspace(ws, plan.workspace_bytes(L.OP_DOUBLE_BACKWARD, N), x)
+        _run("tpconv_linear_double_backward", plan.handle, N, groups._perm, groups._offsets, px, pw, pg, pa, pal, pdg,
+             pdx, pdw, wp, wn, _raw_stream(dev, stream))
+    return {k: v for k, v in (("d_g", d_g), ("d_x", d_x), ("d_weight", d_w)) if v is not None}
 
 
 # ---- layer norm ----------------------------------------------------------------------------------------
 
 
-def _norm_args(plan, x, **t):
-    dev = _cuda_device("x", x)
+def _rows(plan, x):
+    dev = _device_of("x", x)
     if x.dim() != 2:
         raise ValueError(f"x: expected shape (N, {plan.dim}), got {tuple(x.shape)}")
     N = x.shape[0]
-    rows, w, b = (N, plan.dim), (plan.weight_numel,), (plan.bias_numel,)
-    shapes = {"x": rows, "g": rows, "out": rows, "weight": w, "bias": b}
-    _need("x", x, rows, dev)
-    for k, v in t.items():
-        if v is None and k == "g":
-            raise TypeError("g: expected a tensor")
-        _need(k, v, shapes[k[3:] if k.startswith("gg_") else k], dev)
-    return N, dev
+    rows = (N, plan.dim)
+    return N, dev, rows, _ptr("x", x, rows, dev)
 
 
 def norm_forward(plan, x, weight=None, bias=None, out=None, stream=None):
     """The layer norm of x[N, dim]; weight None stands for ones, bias None for zeros."""
-    N, dev = _norm_args(plan, x, weight=weight, bias=bias, out=out)
+    N, dev, rows, px = _rows(plan, x)
+    pw = _ptr("weight", weight, (plan.weight_numel,), dev, True)
+    pb = _ptr("bias", bias, (plan.bias_numel,), dev, True)
     with _on(dev, stream, x, weight, bias):
         if out is None:
-            out = _new(True, (N, plan.dim), dev)
-        L.tpconv_norm_forward(plan, N, x, weight, bias, out, stream)
+            out, po = _new(x, True, *rows)
+        else:
+            po = _ptr("out", out, rows, dev)
+        _run("tpconv_norm_forward", plan.handle, N, px, pw, pb, po, _raw_stream(dev, stream))
     return out
 
 
 def norm_backward(plan, x, weight, g, want=("dx", "dweight", "dbias"), ws=None, stream=None):
     """{"dx", "dweight", "dbias"} for the cotangent g of the output."""
-    N, dev = _norm_args(plan, x, weight=weight, g=g)
+    N, dev, rows, px = _rows(plan, x)
+    pw, pg = _ptr("weight", weight, (plan.weight_numel,), dev, True), _ptr("g", g, rows, dev)
     _wanted(want, ("dx", "dweight", "dbias"))
     with _on(dev, stream, x, weight, g):
-        outs = {"dx": _new("dx" in want, (N, plan.dim), dev),
-                "dweight": _new("dweight" in want, (plan.weight_numel,), dev),
-                "dbias": _new("dbias" in want, (plan.bias_numel,), dev)}
-        ws = _ws_for(ws, L.tpconv_norm_workspace_size(plan, L.OP_BACKWARD, N), dev)
-        L.tpconv_norm_backward(plan, N, x, weight, g, outs["dx"], outs["dweight"], outs["dbias"], ws, stream)
-    return {k: v for k, v in outs.items() if v is not None}
+        dx, pdx = _new(x, "dx" in want, *rows)
+        dw, pdw = _new(x, "dweight" in want, plan.weight_numel)
+        db, pdb = _new(x, "dbias" in want, plan.bias_numel)
+        _ws, wp, wn = _workspace(ws, plan.workspace_bytes(L.OP_BACKWARD, N), x)
+        _run("tpconv_norm_backward", plan.handle, N, px, pw, pg, pdx, pdw, pdb, wp, wn, _raw_stream(dev, stream))
+    return {k: v for k, v in (("dx", dx), ("dweight", dw), ("dbias", db)) if v is not None}
 
 
 def norm_double_backward(plan, x, weight, g, gg_x=None, gg_weight=None, gg_bias=None,
                          want=("d_g", "d_x", "d_weight"), ws=None, stream=None):
     """Gradients of <gg_x, dx> + <gg_weight, dweight> + <gg_bias, dbias> by g, x and weight."""
-    N, dev = _norm_args(plan, x, weight=weight, g=g, gg_x=gg_x, gg_weight=gg_weight, gg_bias=gg_bias)
+    N, dev, rows, px = _rows(plan, x)
+    nw = (plan.weight_numel,)
+    pw, pg = _ptr("weight", weight, nw, dev, True), _ptr("g", g, rows, dev)
+    pa, pal = _ptr("gg_x", gg_x, rows, dev, True), _ptr("gg_weight", gg_weight, nw, dev, True)
+    pbe = _ptr("gg_bias", gg_bias, (plan.bias_numel,), dev, True)
     _wanted(want, ("d_g", "d_x", "d_weight"))
     with _on(dev, stream, x, weight, g, gg_x, gg_weight, gg_bias):
-        outs = {"d_g": _new("d_g" in want, (N, plan.dim), dev), "d_x": _new("d_x" in want, (N, plan.dim), dev),
-                "d_weight": _new("d_weight" in want, (plan.weight_numel,), dev)}
-        ws = _ws_for(ws, L.tpconv_norm_workspace_size(plan, L.OP_DOUBLE_BACKWARD, N), dev)
-        L.tpconv_norm_double_backward(plan, N, x, weight, g, gg_x, gg_weight, gg_bias, outs["d_g"], outs["d_x"],
-                                      outs["d_weight"], ws, stream)
-    return {k: v for k, v in outs.items() if v is not None}
+        d_g, pdg = _new(x, "d_g" in want, *rows)
+        d_x, pdx = _new(x, "d_x" in want, *rows)
+        d_w, pdw = _new(x, "d_weight" in want, plan.weight_numel)
+        _ws, wp, wn = _workspace(ws, plan.workspace_bytes(L.OP_DOUBLE_BACKWARD, N), x)
+        _run("tpconv_norm_double_backward", plan.handle, N, px, pw, pg, pa, pal, pbe, pdg, pdx, pdw, wp, wn,
+             _raw_stream(dev, stream))
+    return {k: v for k, v in (("d_g", d_g), ("d_x", d_x), ("d_weight", d_w)) if v is not None}
 
 
 # ---- torch autograd glue: as for the convolution, the backward of a backward is the library's double
