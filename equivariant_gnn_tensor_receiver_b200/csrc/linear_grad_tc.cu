@@ -4,15 +4,17 @@
 //   dW[t][u][w] = sum over the (node, m) rows of type t of x[n, u, m] g[n, w, m]
 //
 // per path, 128 input channels and 64 output channels: a product whose depth is the
-// ragged row count of the type.  A chunk is the rows of 64, 16, 8 or 8 nodes
-// (l = 0..3: 64, 48, 40, 56 rows); copy threads gather the nodes' pieces of x and g by
-// perm, 16 bytes a thread (4 where a block or tensor is not aligned for it).  The A operand is x transposed: thread u reads its channel of every row (the
+// ragged row count of the type.  A chunk is the rows of 64, 21, 12 or 9 nodes
+// (l = 0..3: 64, 63, 60, 63 rows, filled up with zeros); copy threads gather the nodes'
+// pieces of x and g by perm, 16 bytes a thread (4 where a block or tensor is not aligned
+// for it).  The A operand is x transposed: thread u reads its channel of every row (the
 // lanes of a warp are 2l+1 floats apart: no bank conflicts), splits it (3xTF32) and
 // stores hi and lo to TMEM, lane = u, column = row.  The B operand is g: thread w
-// reads its channel and writes hi and lo into the K-major 128-byte-swizzled tile.  One
-// thread issues A_lo B_hi + A_hi B_lo, then A_hi B_hi.  After kRound chunks the
-// accumulator's bank is added into fp32 registers (round to nearest), which bounds
-// the chain of tensor-core additions whatever the number of rows.
+// reads its channel and writes hi and lo into the K-major 128-byte-swizzled tile, lo
+// as further columns.  One thread issues (D1 | D2) += A_hi (B_hi | B_lo) and
+// D2 += A_lo B_hi.  After kRound chunks the accumulator's bank is added into fp32
+// registers (round to nearest), which bounds the chain of tensor-core additions
+// whatever the number of rows.
 //
 // The (path, channel tile) entries x types x chunks are cut into one equal share per
 // CTA.  A type's rows that lie in one share are stored straight into dW; a share
@@ -22,8 +24,10 @@
 //
 // Bound: HBM (x and g read once), next to shared memory: a row of 64 + 64 channels
 // is 512 B from HBM and about 2.3 KB of shared-memory traffic.
-// Warps 0-3 convert x, 4-7 convert g, 8-11 add finished banks and store, 12-14
-// copy, 15 issues the MMAs.  Waits are bounded as in the row kernel.
+// Two sets of warps convert every second chunk each (the latency of a chunk's steps is
+// what bounds it): warps 0-3 and 8-11 x, 4-7 and 12-15 g; 16-23 add finished banks (32
+// columns each) and store, 24-26 copy, 27 issues the MMAs.  Waits are bounded as in the
+// row kernel.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -43,17 +47,18 @@ __device__ int g_linear_grad_error;  // first code recorded by an expired wait (
 constexpr int kSMs = 148;                     // CTAs of a call, at most
 constexpr int kMT = 128, kNT = 64;            // input and output channels of a tile
 constexpr int kKMax = 64;                     // rows of a chunk, at most
-constexpr int kRound = 3;                     // chunks accumulated in TMEM before they are added up
-constexpr int kBTile = kNT * kKMax * 4;       // 16 KB: hi or lo of a B chunk
-constexpr int kMaxStages = 6;
+constexpr int kRound = 2;                     // chunks accumulated in TMEM before they are added up
+constexpr int kBHalf = 2 * kNT * 128;         // 32 rows of B: 64 columns' hi and behind them their lo
+constexpr int kBTile = 2 * kBHalf;
+constexpr int kMaxStages = 4;                 // raw chunks, an even number
 constexpr int kSMemMax = 227 * 1024;
-constexpr int kThreads = 512;
+constexpr int kThreads = 896;
 constexpr int kCopy = 96;                     // copy threads
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemA = 0, kTmemAStage = 2 * kKMax, kTmemD = 256;
+constexpr uint32_t kTmemA = 0, kTmemAStage = 2 * kKMax, kTmemD = 256, kTmemDStage = 128;  // A: hi | lo, D: D1 | D2
 
 // nodes and rows of a chunk
-__host__ __device__ constexpr int chunk_nodes(int d) { return d == 1 ? 64 : (d == 3 ? 16 : 8); }
+__host__ __device__ constexpr int chunk_nodes(int d) { return kKMax / d; }
 
 // (path, 128 input channels, 64 output channels)
 struct Entry {
@@ -150,47 +155,45 @@ struct Walk {
   }
 };
 
-// thread u: its channel of rows K0 .. K0+7 of the chunk (zeros at and behind kv)
-template <int D, bool WHOLE>
-__device__ __forceinline__ void read8(const float* col, int pitch, int k0, int kv, float (&v)[8]) {
+// 16 rows from K0 of the thread's channel, split (zeros at and behind kv).  The pitch is
+// hidden from the compiler, which would keep a register for every node's offset.
+template <int D, bool SPLIT, bool WHOLE>
+__device__ __forceinline__ void read16(const float* col, int pitch, int k0, int kv, float (&h)[16], float (&l)[16]) {
+  asm volatile("" : "+r"(pitch));
+  const float* row = col + (k0 / D) * pitch;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     const int k = k0 + i;
-    v[i] = (WHOLE || k < kv) ? col[(k / D) * pitch + k % D] : 0.f;
+    const float v = (WHOLE ? k < chunk_nodes(D) * D : k < kv) ? row[k % D] : 0.f;
+    if (k % D == D - 1) row += pitch;
+    tf32_split<SPLIT>(v, h[i], l[i]);
   }
 }
 template <int D, bool SPLIT, bool WHOLE>
 __device__ __forceinline__ void convert_a(const float* col, int pitch, int kv, uint32_t ta) {
-  constexpr int ROWS = chunk_nodes(D) * D;
 #pragma unroll
-  for (int k0 = 0; k0 < ROWS; k0 += 8) {
+  for (int k0 = 0; k0 < kKMax; k0 += 16) {
     if (!WHOLE && k0 >= kv) break;
-    float v[8], h[8];
-    read8<D, WHOLE>(col, pitch, k0, kv, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) tf32_split<SPLIT>(v[i], h[i], v[i]);
-    tmem_st8(ta + k0, h);
-    if (SPLIT) tmem_st8(ta + kKMax + k0, v);
+    float h[16], l[16];
+    read16<D, SPLIT, WHOLE>(col, pitch, k0, kv, h, l);
+    tmem_st16(ta + k0, h);
+    if (SPLIT) tmem_st16(ta + kKMax + k0, l);
   }
 }
-// thread (w, half): every second group of 8 rows of its channel, into the swizzled tile
+// thread (w, half): every second group of 16 rows of its channel, into the swizzled tile
 template <int D, bool SPLIT, bool WHOLE, int HALF>
-__device__ __forceinline__ void convert_b(const float* col, int pitch, int w, int kv, unsigned char* hi) {
-  constexpr int ROWS = chunk_nodes(D) * D;
+__device__ __forceinline__ void convert_b(const float* col, int pitch, int w, int n16, int kv, unsigned char* hi) {
 #pragma unroll
-  for (int k0 = 8 * HALF; k0 < ROWS; k0 += 16) {
+  for (int k0 = 16 * HALF; k0 < kKMax; k0 += 32) {
     if (!WHOLE && k0 >= kv) break;
-    float v[8], h[8];
-    read8<D, WHOLE>(col, pitch, k0, kv, v);
+    float h[16], l[16];
+    read16<D, SPLIT, WHOLE>(col, pitch, k0, kv, h, l);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tf32_split<SPLIT>(v[i], h[i], v[i]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = k0 / 4 + i;  // 16-byte column of the tile
-      const int off = (j >> 3) * (kNT * 128) + w * 128 + (((j & 7) ^ (w & 7)) << 4);
-      *reinterpret_cast<float4*>(hi + off) = make_float4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-      if (SPLIT)
-        *reinterpret_cast<float4*>(hi + kBTile + off) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int i = 0; i < 4; ++i) {
+      const int j = k0 / 4 + i;  // 16-byte column of the tile; the lo rows begin at a multiple of 16
+      unsigned char* to = hi + (j >> 3) * kBHalf + w * 128 + (((j & 7) ^ (w & 7)) << 4);
+      *reinterpret_cast<float4*>(to) = make_float4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+      if (SPLIT) *reinterpret_cast<float4*>(to + n16 * 128) = make_float4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
     }
   }
 }
@@ -206,18 +209,19 @@ __device__ __forceinline__ void chunk_a(const float* raw, int u, int cu, int kv,
 }
 template <int D, bool SPLIT>
 __device__ __forceinline__ void chunk_b(const float* raw, int t, int cw, int kv, unsigned char* hi) {
-  const int w = t & 63;
+  const int w = t & 63, n16 = (cw + 15) & ~15;
+  if (w >= n16) return;
   const float* col = raw + min(w, cw - 1) * D;
   if (kv == chunk_nodes(D) * D) {
     if (t < 64)
-      convert_b<D, SPLIT, true, 0>(col, cw * D, w, kv, hi);
+      convert_b<D, SPLIT, true, 0>(col, cw * D, w, n16, kv, hi);
     else
-      convert_b<D, SPLIT, true, 1>(col, cw * D, w, kv, hi);
+      convert_b<D, SPLIT, true, 1>(col, cw * D, w, n16, kv, hi);
   } else {
     if (t < 64)
-      convert_b<D, SPLIT, false, 0>(col, cw * D, w, kv, hi);
+      convert_b<D, SPLIT, false, 0>(col, cw * D, w, n16, kv, hi);
     else
-      convert_b<D, SPLIT, false, 1>(col, cw * D, w, kv, hi);
+      convert_b<D, SPLIT, false, 1>(col, cw * D, w, n16, kv, hi);
   }
 }
 
@@ -228,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* sB = base;  // 2 x (hi | lo)
-  unsigned char* sRaw = base + 4 * kBTile;
+  unsigned char* sB = base;  // of each set
+  unsigned char* sRaw = base + 2 * kBTile;
   Entry* E = reinterpret_cast<Entry*>(sRaw + stages * stage_bytes);
   int* offs = reinterpret_cast<int*>(E + P.n_entries);
   __shared__ Shared sh;
@@ -248,13 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.afull[i], 256);
       mbar_init(&sh.aempty[i], 1);
       mbar_init(&sh.dfull[i], 1);
-      mbar_init(&sh.dempty[i], 128);
+      mbar_init(&sh.dempty[i], 256);
     }
     mbar_init(&sh.fin, 1);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 15) tmem_alloc(&sh.tmem, kTmemCols);
+  if (warp == 27) tmem_alloc(&sh.tmem, kTmemCols);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -269,16 +273,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   Piece q;
   bool ok = true;
   int ci = 0;  // chunks so far
-  if (warp < 8) {
-    // ---- operands ----
-    const bool is_a = warp < 4;
+  if (warp < 16) {
+    // ---- operands: chunks of the set's parity ----
+    const bool is_a = (warp & 7) < 4;
+    const int set = warp >> 3;
     const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemA;
     const int t = threadIdx.x & 127;
     while (ok && walk.next(&q)) {
       const Entry& L = E[q.e];
       const int d = L.d, cu = L.cu, cw = L.cw, nq = chunk_nodes(d);
       for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-        const int st = ci % stages, ab = ci & 1, kv = min(nq, q.nodes - n0) * d;
+        if ((ci & 1) != set) continue;
+        const int st = ci % stages, ab = set, kv = min(nq, q.nodes - n0) * d;
         if (ci >= 2 && !wait(&sh.aempty[ab], ((ci >> 1) + 1) & 1, limit, abort, 1)) ok = false;
         if (ok && !wait(&sh.full[st], (ci / stages) & 1, limit, abort, 2)) ok = false;
         if (!ok) break;
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after_sync();
           const float* rx = reinterpret_cast<const float*>(raw);
           const uint32_t ta = lane_base + ab * kTmemAStage;
-          if (warp * 32 < cu) {  // (rows of the product behind the channels are not stored)
+          if ((warp & 3) * 32 < cu) {  // (rows of the product behind the channels are not stored)
             switch (d) {
               case 1: chunk_a<1, SPLIT>(rx, t, cu, kv, ta); break;
               case 3: chunk_a<3, SPLIT>(rx, t, cu, kv, ta); break;
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_before_sync();
         } else {
           const float* rg = reinterpret_cast<const float*>(raw + g_offset);
-          unsigned char* hi = sB + ab * 2 * kBTile;
+          unsigned char* hi = sB + ab * kBTile;
           switch (d) {
             case 1: chunk_b<1, SPLIT>(rg, t, cw, kv, hi); break;
             case 3: chunk_b<3, SPLIT>(rg, t, cw, kv, hi); break;
@@ -313,18 +319,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh.afull[ab]);
       }
     }
-  } else if (warp < 12) {
-    // ---- finished banks to registers, pieces to memory ----
-    const int r = threadIdx.x - 256;
+  } else if (warp < 24) {
+    // ---- finished banks to registers, pieces to memory: a row and 32 columns a thread ----
+    const int r = threadIdx.x & 127, c0 = 32 * ((warp - 16) >> 2);
     const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kTmemD;
     int ri = 0;  // rounds so far
     while (ok && walk.next(&q)) {
       const Entry& L = E[q.e];
       const int cu = L.cu, cw = L.cw, nq = chunk_nodes(L.d);
       const int rounds = ((q.nodes + nq - 1) / nq + kRound - 1) / kRound;
-      float acc[kNT];
+      const bool mine = (warp & 3) * 32 < cu && c0 < cw;
+      float acc[32];
 #pragma unroll
-      for (int i = 0; i < kNT; ++i) acc[i] = 0.f;
+      for (int i = 0; i < 32; ++i) acc[i] = 0.f;
       for (int k = 0; k < rounds; ++k, ++ri) {
         const int db = ri & 1;
         if (!wait(&sh.dfull[db], (ri >> 1) & 1, limit, abort, 3)) {
@@ -332,30 +339,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         fence_after_sync();
-        if ((warp & 3) * 32 < cu) {
+        if (mine) {
+          const uint32_t td = lane_base + db * kTmemDStage + c0;
 #pragma unroll
-          for (int c = 0; c < kNT; c += 16) {
-            if (c < cw) {
+          for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {
               float v[16];
-              tmem_ld16(lane_base + db * kNT + c, v);
+              tmem_ld16(td + p * ((cw + 15) & ~15) + c, v);
 #pragma unroll
               for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
             }
-          }
         }
         fence_before_sync();
         mbar_arrive(&sh.dempty[db]);
       }
-      if (!ok || r >= cu) continue;
+      if (!ok || !mine || r >= cu) continue;
       if (q.slot >= 0) {  // a partial tile has room for all columns
-        float4* dst = reinterpret_cast<float4*>(part + (int64_t(q.slot) * kMT + r) * kNT);
+        float4* dst = reinterpret_cast<float4*>(part + (int64_t(q.slot) * kMT + r) * kNT + c0);
 #pragma unroll
-        for (int i = 0; i < kNT; i += 4) dst[i / 4] = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        for (int i = 0; i < 32; i += 4) dst[i / 4] = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
       } else {
-        float* dst = P.dw + int64_t(q.t) * P.wnumel + L.woff + int64_t(r) * L.co;
+        float* dst = P.dw + int64_t(q.t) * P.wnumel + L.woff + int64_t(r) * L.co + c0;
 #pragma unroll
-        for (int i = 0; i < kNT; i += VEC) {
-          if (i < cw) {
+        for (int i = 0; i < 32; i += VEC) {
+          if (c0 + i < cw) {
             if constexpr (VEC == 4)
               *reinterpret_cast<float4*>(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
             else
@@ -364,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 15) {
+  } else if (warp < 27) {
     // ---- node rows to shared memory, several chunks ahead ----
-    const int r = threadIdx.x - 384;
+    const int r = threadIdx.x - 768;
     while (walk.next(&q)) {  // (a warp that gave up keeps passing the group's barriers)
       const Entry& L = E[q.e];
       const int d = L.d, nq = chunk_nodes(d), lx = L.cu * d, lg = L.cw * d;
@@ -404,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(&q)) {
       const Entry& L = E[q.e];
       const int d = L.d, nq = chunk_nodes(d);
-      const uint32_t idesc = idesc_tf32(kMT, (L.cw + 15) & ~15);
+      const int n16 = (L.cw + 15) & ~15;
+      const uint32_t id1 = idesc_tf32(kMT, SPLIT ? 2 * n16 : n16), id2 = idesc_tf32(kMT, n16);
       int in_round = 0;
       for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
         const int ab = ci & 1, db = ri & 1, steps = (min(nq, q.nodes - n0) * d + 7) / 8;
@@ -414,24 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after_sync();
         const bool last = ++in_round == kRound || n0 + nq >= q.nodes;
         if (lane == 0) {
-          const uint32_t td = tmem + kTmemD + db * kNT, a = tmem + kTmemA + ab * kTmemAStage;
-          const uint64_t bh = sw128_kmajor(smem_u32(sB + ab * 2 * kBTile)),
-                         bl = sw128_kmajor(smem_u32(sB + ab * 2 * kBTile + kBTile));
-          auto step = [](int k) { return uint64_t((k >> 2) * (kNT * 128 / 16) + (k & 3) * 2); };
-          uint32_t acc = in_round > 1;
-          if (SPLIT) {
-#pragma unroll
-            for (int k = 0; k < kKMax / 8; ++k) {
-              if (k >= steps) break;
-              mma_tf32_ta(td, a + kKMax + 8 * k, bh + step(k), idesc, k > 0 ? 1u : acc);
-              mma_tf32_ta(td, a + 8 * k, bl + step(k), idesc, 1);
-            }
-            acc = 1;
-          }
+          const uint32_t td = tmem + kTmemD + db * kTmemDStage, a = tmem + kTmemA + ab * kTmemAStage;
+          const uint64_t b = sw128_kmajor(smem_u32(sB + ab * kBTile));
 #pragma unroll
           for (int k = 0; k < kKMax / 8; ++k) {
             if (k >= steps) break;
-            mma_tf32_ta(td, a + 8 * k, bh + step(k), idesc, k > 0 ? 1u : acc);
+            const uint64_t bk = b + uint64_t((k >> 2) * (kBHalf / 16) + (k & 3) * 2);
+            mma_tf32_ta(td, a + 8 * k, bk, id1, in_round > 1 || k > 0);
+            if (SPLIT) mma_tf32_ta(td + n16, a + kKMax + 8 * k, bk, id2, 1);
           }
           mma_commit(&sh.aempty[ab]);
           if (last) mma_commit(&sh.dfull[db]);
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 15) {
+  if (warp == 27) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -484,19 +483,22 @@ __global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant_
       int64_t seg = int64_t(count_units(offs, t, unit)) * c;  // cost before the type's first chunk
       for (int k = 0; k < e; ++k) seg += int64_t(total[P.e[k].d >> 1]) * P.e[k].cost;
       const int64_t end = seg + int64_t(n - 1) * c;  // cost before its last chunk
+      // the shares that hold the first and the last chunk
+      const int64_t per = div_cost(all, ctas), more = all - per * ctas, wide = more * (per + 1);
+      auto owner = [&](int64_t x) {
+        return x < wide ? int(div_cost(x, int(per + 1))) : int(more + div_cost(x - wide, int(max(per, int64_t(1)))));
+      };
+      const int first = owner(seg), last = owner(end);
       m = 0;
-      for (int b0 = 0; b0 < ctas; b0 += 32) {
+      for (int b0 = first; b0 <= last; b0 += 32) {
         const int b = b0 + threadIdx.x;
-        bool has = false, first = false;
-        if (b < ctas) {
-          const int64_t lo = share_begin(all, b, ctas), hi = share_begin(all, b + 1, ctas);
-          first = lo <= seg && seg < hi;
-          // the first chunk of the type at or behind lo, if it is in the share
-          const int64_t x = lo <= seg ? seg : seg + div_cost(lo - seg + c - 1, c) * c;
-          has = x <= end && x < hi;
+        bool has = b == first;
+        if (b > first && b <= last) {  // a share narrower than a chunk's cost may hold none
+          const int64_t lo = per * b + min(int64_t(b), more), hi = per * (b + 1) + min(int64_t(b + 1), more);
+          has = seg + div_cost(lo - seg + c - 1, c) * c < hi;
         }
         const unsigned mask = __ballot_sync(0xffffffffu, has);
-        if (has) slot[m + __popc(mask & ((1u << threadIdx.x) - 1))] = 2 * b + first;
+        if (has) slot[m + __popc(mask & ((1u << threadIdx.x) - 1))] = 2 * b + (b == first);
         m += __popc(mask);
       }
       if (m == 1) m = -1;  // all in one share: stored by its CTA
@@ -564,8 +566,8 @@ cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t l
         E.d = L.d, E.xoff = L.xoff + u0 * L.d, E.goff = L.goff + w0 * L.d;
         E.cu = std::min(kMT, L.ci - u0), E.cw = std::min(kNT, L.co - w0), E.co = L.co;
         E.woff = L.woff + int64_t(u0) * L.co + w0;
-        // the KB that a chunk moves, at least the rows that it converts
-        E.cost = 8 + std::max((E.cu + E.cw) * L.d * chunk_nodes(L.d) / 256, L.d * chunk_nodes(L.d) / 4);
+        // the KB that a chunk moves, and what any chunk takes
+        E.cost = 16 + (E.cu + E.cw) * L.d * chunk_nodes(L.d) / 256;
         P.coef[L.d >> 1] += E.cost;
         sx = std::max(sx, E.cu * L.d * chunk_nodes(L.d) * 4);
         sg = std::max(sg, E.cw * L.d * chunk_nodes(L.d) * 4);
@@ -573,8 +575,10 @@ cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t l
   }
   sx = (sx + 15) & ~15;
   const int stage = (sx + sg + 15) & ~15;
-  const int fixed = 1024 + 4 * kBTile + P.n_entries * int(sizeof(Entry)) + (P.T + 2) * 4;
-  const int stages = std::min(kMaxStages, (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / stage);
+  const int fixed = 1024 + 2 * kBTile + P.n_entries * int(sizeof(Entry)) + (P.T + 2) * 4;
+  // at most 32 KB of x and 16 KB of g: two stages always fit; an even number, so that a stage
+  // belongs to one set of converters
+  const int stages = std::min(kMaxStages, (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / stage) & ~1;
   if (stages < 2) return cudaErrorInvalidValue;
   const int sm = fixed + stages * stage;
   const bool v = vec4(G);
