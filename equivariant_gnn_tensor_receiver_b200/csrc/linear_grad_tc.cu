@@ -453,10 +453,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// One (entry, type) per blockIdx.x, kJoinRows input channels per blockIdx.y: zeros
+// One (entry, type) per blockIdx.x, 16 input channels per blockIdx.y: zeros
 // for a type without nodes, the sum of the partial tiles in CTA order for one whose
 // rows are spread over several shares, nothing otherwise.
-constexpr int kJoinRows = 16;
+constexpr int kJoinRows = 16;  // 16 float4 of 64 columns a row: 256 threads
+static_assert(kJoinRows * kNT / 4 == 256, "one float4 a thread");
 __global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant__ Params P, int ctas,
                                                           const float* __restrict__ part) {
   __shared__ int offs[TPCONV_MAX_TYPES + 2];
@@ -508,15 +509,21 @@ __global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant_
   __syncthreads();
   const int m = s_slots;
   if (m < 0) return;
-  float* dw = P.dw + int64_t(t) * P.wnumel + L.woff;
-  for (int i = threadIdx.x; i < (r1 - r0) * cw; i += 256) {
-    const int r = r0 + i / cw, w = i % cw;
-    const float* p0 = part + int64_t(r) * kNT + w;
-    float s = 0.f;
+  // a float4 of the partial tiles a thread (their rows have room for 64 columns)
+  const int r = r0 + (threadIdx.x >> 4), w = 4 * (threadIdx.x & 15);
+  if (r >= r1 || w >= cw) return;
+  const float* p0 = part + int64_t(r) * kNT + w;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int b = 0; b < m; ++b) s += p0[int64_t(slot[b]) * kMT * kNT];
-    dw[int64_t(r) * L.co + w] = s;
+  for (int b = 0; b < m; ++b) {
+    const float4 v = *reinterpret_cast<const float4*>(p0 + int64_t(slot[b]) * kMT * kNT);
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
+  float* dw = P.dw + int64_t(t) * P.wnumel + L.woff + int64_t(r) * L.co + w;
+  dw[0] = s.x;
+  if (w + 1 < cw) dw[1] = s.y;
+  if (w + 2 < cw) dw[2] = s.z;
+  if (w + 3 < cw) dw[3] = s.w;
 }
 
 int tiles_u(const LinPath& p) { return (p.ci + kMT - 1) / kMT; }
