@@ -387,18 +387,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r < 64) nodes[r] = (node >= 0 && node < P.N) ? node : 0;
         asm volatile("bar.sync 1, 96;" ::: "memory");
         node = r < nq && n0 + nq + r < q.nodes ? P.perm[q.first + n0 + nq + r] : 0;
+        if (r < 2) prefetch_nodes(P.perm, q.first + n0 + kPermAhead + 32 * r, P.N);
         if (ok && ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
         if (!ok) continue;
         const uint32_t dst = smem_u32(sRaw + st * stage_bytes);
         auto rows = [&](const float* src, int dim, int len, uint32_t to0) {
           const int n = len / VEC;
           const RowShare w(n, r, kCopy);
-          for (int o = w.at; o < n; o += w.pieces) {
-            uint32_t to = to0 + (w.row * len + o * VEC) * 4;
-#pragma unroll 4
-            for (int k = w.row; k < cnt; k += w.rows, to += w.rows * len * 4)
-              copy_async<VEC>(to, src + o * VEC + int64_t(nodes[k]) * dim);
-          }
+          for (int o = w.at; o < n; o += w.pieces)
+            copy_rows<VEC>(src + o * VEC, dim, nodes, w, cnt, to0 + (w.row * len + o * VEC) * 4, len * 4);
         };
         rows(x, P.dim_x, lx, dst);
         rows(g, P.dim_g, lg, dst + g_offset);

@@ -43,6 +43,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "linear_tc.h"
 #include "linear_tc_common.cuh"
@@ -240,9 +241,19 @@ __device__ __forceinline__ void lay_out(uint32_t td, float* stage, int r, int nw
   }
 }
 
+struct One {
+  float x;
+  __device__ __forceinline__ One operator+(const One& o) const { return {x + o.x}; }
+};
+struct __align__(16) Four {
+  float x, y, z, w;
+  __device__ __forceinline__ Four operator+(const Four& o) const { return {x + o.x, y + o.y, z + o.z, w + o.w}; }
+};
+
 template <bool SPLIT, int VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_tc(const __grid_constant__ Params P, int halves, int stages, uint64_t limit) {
+  using Pack = std::conditional_t<VEC == 4, Four, One>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -434,24 +445,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = w.at; o < n; o += w.pieces) {
           const float* src = stage + w.row * pitch + o * VEC;
           float* out = P.out + O.off + o * VEC;
-#pragma unroll 4
-          for (int q = w.row; q < it.count; q += w.rows, src += w.rows * pitch) {
-            const int m = nodes[q];
-            float* dst = out + int64_t(m) * dim;
-            if constexpr (VEC == 4) {
-              float4 v = it.zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(src);
-              if (m >= 0) {
-                if (P.accumulate) {
-                  const float4 u = *reinterpret_cast<const float4*>(dst);
-                  v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
-                }
-                *reinterpret_cast<float4*>(dst) = v;
+          // Four rows at a time, read before any is stored: the compiler cannot tell the
+          // stores from the reads, and would wait for each.
+          auto put = [&](int m, Pack v) {
+            if (m < 0) return;
+            Pack* dst = reinterpret_cast<Pack*>(out + int64_t(m) * dim);
+            if (P.accumulate) v = v + *dst;
+            *dst = v;
+          };
+          int q = w.row;
+          const int rp = w.rows * pitch;
+          if (!it.zero)
+            for (; q + 3 * w.rows < it.count; q += 4 * w.rows, src += 4 * rp) {
+              int m[4];
+              Pack v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                m[i] = nodes[q + i * w.rows];
+                v[i] = *reinterpret_cast<const Pack*>(src + i * rp);
               }
-            } else {
-              const float v = it.zero ? 0.f : *src;
-              if (m >= 0) *dst = P.accumulate ? *dst + v : v;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) put(m[i], v[i]);
             }
-          }
+          for (; q < it.count; q += w.rows, src += rp)
+            put(nodes[q], it.zero ? Pack{} : *reinterpret_cast<const Pack*>(src));
         }
       }
     }
@@ -477,7 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ni;
       if (r < 128) nodes[r] = (node >= 0 && node < P.N) ? node : 0;  // (a wrong node's row is not stored)
       more = next_item(&it);
-      if (more) node = node_of(it);  // read while this tile is copied
+      if (more) {
+        node = node_of(it);  // read while this tile is copied
+        if (r < 4) prefetch_nodes(P.perm, it.first + kPermAhead + 32 * r, P.N);
+      }
       asm volatile("bar.sync 3, 160;" ::: "memory");
       for (int s = 0; ok && s < O.count; ++s) {
         const LinSource& Q = S[O.first + s];
@@ -492,9 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int o = w.at; o < n; o += w.pieces) {
             const float* src = x + k0 * O.d + o * VEC;
             uint32_t to = dst + (w.row * pitch + o * VEC) * 4;
-#pragma unroll 4
-            for (int q = w.row; q < cur.count; q += w.rows, to += w.rows * pitch * 4)
-              copy_async<VEC>(to, src + int64_t(nodes[q]) * P.dim_src);
+            copy_rows<VEC>(src, P.dim_src, nodes, w, cur.count, to, pitch * 4);
           }
           copies_arrive(&sh.full[set][st]);
         }

@@ -66,6 +66,13 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Brings the node ids some tiles ahead into L2: a tile is copied in less time than HBM
+// answers, so that reading them one tile ahead alone would bound the copies.
+constexpr int kPermAhead = 512;
+__device__ __forceinline__ void prefetch_nodes(const int* perm, int at, int64_t N) {
+  if (at < N) asm volatile("prefetch.global.L2 [%0];" ::"l"(perm + at));
+}
+
 // How `threads` threads share rows of `n` pieces: as many whole rows at a time as
 // fit (or, for longer rows, the pieces of one row in turn); a thread keeps its place
 // in the row, so that a step costs an addition and not a division.
@@ -81,6 +88,22 @@ struct RowShare {
     if (row >= rows) at = n;  // a thread left over
   }
 };
+
+// one piece of rows w.row, w.row + w.rows, ... < count: row q of node nodes[q] at src (+ its
+// node's offset) to to + (q - w.row) pitch bytes; the ids of four rows are read at a time, as
+// no read is moved across a copy
+template <int VEC>
+__device__ __forceinline__ void copy_rows(const float* src, int dim, const int* nodes, const RowShare& w, int count,
+                                          uint32_t to, int pitch) {
+  for (int q = w.row; q < count; q += 4 * w.rows, to += 4 * w.rows * pitch) {
+    int n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = q + i * w.rows < count ? nodes[q + i * w.rows] : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n[i] >= 0) copy_async<VEC>(to + i * w.rows * pitch, src + int64_t(n[i]) * dim);
+  }
+}
 
 __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
   uint32_t ok;
