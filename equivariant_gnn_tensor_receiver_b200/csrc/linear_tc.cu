@@ -6,9 +6,9 @@
 // A tile is the (node, m) rows of up to 128 / (2l+1) nodes of one type, times 64
 // output channels.  The weight of the (block, columns, type) is resident in shared
 // memory, split once into TF32 hi and lo; the node rows are the only stream:
-//   copy threads gather the nodes' contiguous pieces [64 channels][2l+1] by perm, 16
-//   bytes a thread (4 where a block or tensor is not aligned for it), several chunks
-//   ahead;
+//   copy warps gather the nodes' contiguous pieces [64 channels][2l+1] by perm, a bulk
+//   copy a node (4-byte asynchronous copies where a block or tensor is not 16-byte
+//   aligned), several chunks ahead;
 //   converter threads, one per row, read their row's channels (stride 2l+1), split
 //   them (3xTF32, Ootomo & Yokota, 2022) and store hi and lo as the A operand in
 //   TMEM: the transposition from [channel][m] to rows costs one shared-memory read
@@ -16,8 +16,8 @@
 //   one thread issues, 8 channels a step, (D1 | D2) += A_hi (B_hi | B_lo) as one product
 //   of up to 128 columns, and D2 += A_lo B_hi: two instructions instead of three, and
 //   the small products add up among themselves;
-//   epilogue threads, one per row and 32 columns, lay D1 + D2 out as [channel][m] in
-//   shared memory, and store the nodes' pieces, 16 bytes a thread.
+//   epilogue threads, one per row, lay D1 + D2 out as [channel][m] in shared memory, and
+//   bulk copies store the nodes' pieces (threads, where they are not aligned or added).
 // The pitch of a node in shared memory is 4 or 8 floats off a multiple of 32, which
 // leaves at most two rows of a warp on a bank.
 //
@@ -32,9 +32,10 @@
 // slots, so two pipelines take every second tile each, with buffers and barriers of
 // their own, and share the weight: warps 0-3 and 4-7 convert, 8-11 and 12-15 run the
 // epilogue, 21 and 22 issue the MMAs; 16-20 copy for both.
-// (Bulk copies of a node's piece were tried in place of the copy threads: about 60
-// cycles of issue a copy, 2.5 times the time at 64 scalars a node.  Both warpgroups of
-// a role on one tile: 340 us against 306 at 262144 nodes of 64x0e+64x1o+64x2e.)
+// (Issuing a bulk copy takes some 60 cycles, so the nodes are dealt out over the warps.
+// Stores from registers held four warps for 5500 cycles a tile, waiting for the memory
+// pipe to take them: 306 us against 270 at 262144 nodes of 64x0e+64x1o+64x2e; both
+// warpgroups of a role on one tile: 340 us.)
 // A sum over more than 160 channels runs in several passes that add to the output.
 // Every wait is bounded by the call's limit; on expiry the kernel records it, stops
 // issuing, waits (bounded) for its own copies and MMAs, frees TMEM and returns.
@@ -64,7 +65,7 @@ constexpr int kMaxHalves = 5;                 // of a resident weight: 160 chann
 constexpr int kRaw = 32928;                   // a raw chunk or an output tile (see node_pitch)
 constexpr int kMaxStages = 2;                 // raw chunks of a pipeline
 constexpr int kSMemMax = 227 * 1024;
-constexpr int kThreads = 736, kCopy = 160;     // copy threads: whole rows of 16, 48, 80, 112 pieces fill them
+constexpr int kThreads = 736, kCopyWarps = 5, kCopy = 32 * kCopyWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemA = 0, kTmemAStage = 128, kTmemD = 256, kTmemDStage = 128;  // A: 2 x (hi 64 | lo 64), D: 2 x (D1 | D2)
 
@@ -105,16 +106,16 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int total[4];                    // tiles of all types for d = 1, 3, 5, 7
+  WalkState walk[kThreads / 32];
   int node_in[2][128], node_out[2][128];
+  int issued[2][kCopyWarps];
 };
 
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, uint64_t limit, volatile int* abort, int code) {
   return wait_or_abort(b, parity, limit, abort, &g_linear_error, code);
 }
 
-// ---- the CTA's share of the work -------------------------------------------------
-// Entries in order, in each the tiles of the types; CTA b owns the tiles whose cost
-// begins in its share.  Every warp walks the same list.
+// ---- the CTA's tiles ---------------------------------------------------------------
 struct Item {
   int e, t, first, count;
   bool run;       // the first tile with this weight
@@ -123,63 +124,29 @@ struct Item {
 };
 
 struct Walk {
+  WalkState* w;
   const Entry* E;
-  const int* offs;
-  const int* total;
-  int n_entries, T;
-  int64_t lo, hi, base = 0;
-  int left = 0;                // tiles of this share left in the entry
-  int e = -1, unit = 1, t = 0;
-  int at = 0, end = 0;         // the group's next node, its end
-  bool fresh = true, empty = false;
+  const Cut* cuts;
+  const int *total, *offs;
+  int n, T;
+  int e = 0, t = 0, at = 0, end = 0, unit = 1;
+  bool zero = false;
 
-  __device__ Walk(const Params& P, const Entry* entries, const int* o, const int* tot)
-      : E(entries), offs(o), total(tot), n_entries(P.n_entries), T(P.T) {
-    int64_t c = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c += int64_t(tot[i]) * P.coef[i];
-    lo = share_begin(c, blockIdx.x, gridDim.x);
-    hi = share_begin(c, blockIdx.x + 1, gridDim.x);
-  }
-  __device__ bool next_entry() {
-    for (;;) {
-      if (e >= 0) base += int64_t(total[E[e].d >> 1]) * E[e].cost;
-      if (++e >= n_entries || base >= hi) {
-        e = n_entries;
-        return false;
-      }
-      const int c = E[e].cost;
-      const int64_t n = total[E[e].d >> 1];
-      const int64_t a = lo <= base ? 0 : min(div_cost(lo - base + c - 1, c), n),
-                    b = min(div_cost(hi - base + c - 1, c), n);
-      if (a < b) {
-        left = int(b - a);
-        unit = tile_of(E[e].d);
-        empty = E[e].count == 0;
-        int j;
-        seek_unit(offs, T, unit, a, &t, &j);
-        end = t < T ? offs[t + 1] : 0;
-        at = t < T ? offs[t] + j * unit : 0;
-        fresh = true;
-        return true;
-      }
+  __device__ __forceinline__ bool next(Item* it) {
+    const bool fresh = at >= end;
+    if (fresh) {
+      const Run r = next_run(w, cuts, n, total, offs, T);
+      if (r.e < 0) return false;
+      e = r.e, t = r.t, at = r.first, end = r.end;
+      unit = cuts[e].nodes;
+      zero = E[e].count == 0;
     }
-  }
-  __device__ bool next(Item* it) {
-    if (left == 0 && !next_entry()) return false;
-    while (at >= end) {
-      if (t + 1 >= T) return false;
-      ++t, fresh = true;
-      at = offs[t], end = offs[t + 1];
-    }
-    it->e = e, it->t = t;
-    it->first = at;
+    it->e = e, it->t = t, it->first = at;
     it->count = min(unit, end - at);
     it->run = fresh;
-    it->zero = empty;
-    fresh = false;
-    at += unit, --left;
-    it->run_last = left == 0 || at >= end;
+    it->zero = zero;
+    at += unit;
+    it->run_last = at >= end;
     return true;
   }
 };
@@ -262,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sOut = sRaw + 2 * stages * (kRaw / 4);
   LinSource* S = reinterpret_cast<LinSource*>(sOut + 2 * (kRaw / 4));
   Entry* E = reinterpret_cast<Entry*>(S + P.n_src);
-  int* offs = reinterpret_cast<int*>(E + P.n_entries);
+  Cut* cuts = reinterpret_cast<Cut*>(E + P.n_entries);
+  int* offs = reinterpret_cast<int*>(cuts + P.n_entries);
   __shared__ Shared sh;
   volatile int* abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -272,11 +240,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     reinterpret_cast<int*>(S)[i] = reinterpret_cast<const int*>(P.s)[i];
   for (int i = threadIdx.x; i < P.n_entries * int(sizeof(Entry) / 4); i += kThreads)
     reinterpret_cast<int*>(E)[i] = reinterpret_cast<const int*>(P.e)[i];
+  if (threadIdx.x < P.n_entries) {
+    const int d = P.e[threadIdx.x].d;
+    cuts[threadIdx.x] = {P.e[threadIdx.x].cost, tile_of(d), d >> 1};
+  }
   load_offsets(offs, P.offsets, P.T, P.N);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       for (int s = 0; s < kMaxStages; ++s) {
-        mbar_init(&sh.full[i][s], kCopy);
+        mbar_init(&sh.full[i][s], VEC == 4 ? kCopyWarps : kCopy);
         mbar_init(&sh.empty[i][s], 128);
       }
       mbar_init(&sh.afull[i], 128);
@@ -301,7 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  Walk walk(P, E, offs, sh.total);
+  {
+    int64_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c += int64_t(sh.total[i]) * P.coef[i];
+    walk_begin(&sh.walk[warp], c);
+  }
+  Walk walk{&sh.walk[warp], E, cuts, sh.total, offs, P.n_entries, P.T};
   Item it;
   // the weight of a run, by the converter and epilogue threads: thread (n, q0) takes four channels at a time
   auto load_weight = [&](const Entry& O, int t) {
@@ -418,12 +396,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // bulk copies of whole pieces (16-byte aligned ones, stored and not added): the warps of the set
+    // take every fourth node each
+    const bool bulk = VEC == 4 && !P.accumulate;
+    const int mine = bulk ? lane * 4 + (warp & 3) : r;
+    auto node_of = [&](const Item& q) { return mine < q.count ? P.perm[q.first + mine] : -1; };
     int d;
-    while (next_item(&d)) {
-      const Entry& O = E[it.e];
-      const int node = r < it.count ? P.perm[it.first + r] : -1;
+    bool more = next_item(&d);
+    int node = more ? node_of(it) : -1;
+    while (more) {
+      const Item cur = it;
+      const Entry& O = E[cur.e];
+      if (bulk) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       bar();  // the set's last tile has been read
-      if (!it.zero) {
+      if (!cur.zero) {
         if (ok) ok = wait(&sh.dfull[set], (d >> 1) & 1, limit, abort, 4);
         if (ok) {
           fence_after_sync();
@@ -437,9 +423,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sh.dempty[set]);
         }
       }
-      nodes[r] = (node >= 0 && node < P.N) ? node : -1;
+      const int out_node = (node >= 0 && node < P.N) ? node : -1;
+      if (bulk) {
+        if (cur.zero)
+          for (int i = r; i < tile_of(O.d) * node_pitch(O.d) / 4; i += 128)
+            reinterpret_cast<float4*>(stage)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      } else {
+        nodes[r] = out_node;
+      }
       bar();
-      if (ok) {
+      if (bulk) {
+        if (ok && out_node >= 0)
+          bulk_store(P.out + int64_t(out_node) * P.dim_out + O.off, smem_u32(stage + mine * node_pitch(O.d)),
+                     uint32_t(O.nw * O.d * 4));
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      more = next_item(&d);
+      if (more) node = node_of(it);  // read while this tile is stored
+      if (ok && !bulk) {
         const int pitch = node_pitch(O.d), dim = P.dim_out, n = O.nw * O.d / VEC;
         const RowShare w(n, r, 128);
         for (int o = w.at; o < n; o += w.pieces) {
@@ -455,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           int q = w.row;
           const int rp = w.rows * pitch;
-          if (!it.zero)
-            for (; q + 3 * w.rows < it.count; q += 4 * w.rows, src += 4 * rp) {
+          if (!cur.zero)
+            for (; q + 3 * w.rows < cur.count; q += 4 * w.rows, src += 4 * rp) {
               int m[4];
               Pack v[4];
 #pragma unroll
@@ -467,14 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) put(m[i], v[i]);
             }
-          for (; q < it.count; q += w.rows, src += rp)
-            put(nodes[q], it.zero ? Pack{} : *reinterpret_cast<const Pack*>(src));
+          for (; q < cur.count; q += w.rows, src += rp)
+            put(nodes[q], cur.zero ? Pack{} : *reinterpret_cast<const Pack*>(src));
         }
       }
     }
+    if (bulk) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (warp < 21) {
     // ---- node rows to shared memory, several chunks ahead ----
-    const int r = threadIdx.x - 512;
     int ci[2] = {0, 0}, ni = 0;  // chunks of each pipeline, tiles
     bool ok = true, more = false;
     auto next_item = [&](Item* q) {  // the next tile with a product
@@ -483,42 +485,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (m && q->zero);
       return m;
     };
-    auto node_of = [&](const Item& q) { return r < q.count ? P.perm[q.first + r] : 0; };
-    more = next_item(&it);
-    int node = more ? node_of(it) : 0;
-    while (more) {  // (a warp that gave up keeps passing the group's barriers)
-      const Item cur = it;
-      const Entry& O = E[cur.e];
-      const int set = ni & 1;
-      int* nodes = sh.node_in[set];
-      ++ni;
-      if (r < 128) nodes[r] = (node >= 0 && node < P.N) ? node : 0;  // (a wrong node's row is not stored)
+    if constexpr (VEC == 4) {
+      // a bulk copy per node, every fifth node a warp: issuing one takes some 60 cycles
+      const int w = warp - 16, r = lane * kCopyWarps + w;
+      auto node_of = [&](const Item& q) {
+        const int n = r < q.count ? P.perm[q.first + r] : 0;
+        return n >= 0 && n < P.N ? n : 0;  // (a wrong node's row is not stored)
+      };
       more = next_item(&it);
-      if (more) {
-        node = node_of(it);  // read while this tile is copied
-        if (r < 4) prefetch_nodes(P.perm, it.first + kPermAhead + 32 * r, P.N);
-      }
-      asm volatile("bar.sync 3, 160;" ::: "memory");
-      for (int s = 0; ok && s < O.count; ++s) {
-        const LinSource& Q = S[O.first + s];
-        const float* x = P.x[Q.pair] + Q.off;
-        for (int k0 = 0; k0 < Q.k; k0 += kKC) {
-          const int c = set ? ci[1]++ : ci[0]++, st = c % stages, pitch = node_pitch(O.d);
-          if (c >= stages && !wait(&sh.empty[set][st], ((c / stages) + 1) & 1, limit, abort, 5)) ok = false;
-          if (!ok) break;
-          const uint32_t dst = smem_u32(sRaw + (set * stages + st) * (kRaw / 4));
-          const int n = min(kKC, Q.k - k0) * O.d / VEC;
-          const RowShare w(n, r, kCopy);
-          for (int o = w.at; o < n; o += w.pieces) {
-            const float* src = x + k0 * O.d + o * VEC;
-            uint32_t to = dst + (w.row * pitch + o * VEC) * 4;
-            copy_rows<VEC>(src, P.dim_src, nodes, w, cur.count, to, pitch * 4);
+      int node = more ? node_of(it) : 0;
+      while (ok && more) {
+        const Item cur = it;
+        const Entry& O = E[cur.e];
+        const int set = ni++ & 1, pitch = node_pitch(O.d) * 4;
+        const int64_t row = int64_t(node) * P.dim_src;
+        more = next_item(&it);
+        if (more) {
+          node = node_of(it);  // read while this tile is copied
+          if (r < 4) prefetch_nodes(P.perm, it.first + kPermAhead + 32 * r, P.N);
+        }
+        const uint32_t mine = cur.count > w ? uint32_t(cur.count - w + kCopyWarps - 1) / kCopyWarps : 0;
+        for (int s = 0; ok && s < O.count; ++s) {
+          const LinSource& Q = S[O.first + s];
+          const float* x = P.x[Q.pair] + row + Q.off;
+          for (int k0 = 0; k0 < Q.k; k0 += kKC) {
+            const int c = ci[set], st = c % stages;
+            const uint32_t bytes = uint32_t(min(kKC, Q.k - k0) * O.d * 4);
+            if (c >= stages && !wait(&sh.empty[set][st], ((c / stages) + 1) & 1, limit, abort, 5)) ok = false;
+            if (!ok) break;
+            ci[set] = c + 1;
+            if (lane == 0) mbar_expect_tx(&sh.full[set][st], bytes * mine);
+            __syncwarp();
+            if (r < cur.count)
+              bulk_load(smem_u32(sRaw + (set * stages + st) * (kRaw / 4)) + r * pitch, x + k0 * O.d, bytes,
+                        &sh.full[set][st]);
           }
-          copies_arrive(&sh.full[set][st]);
         }
       }
+      if (lane == 0) sh.issued[0][w] = ci[0], sh.issued[1][w] = ci[1];
+      asm volatile("bar.sync 3, 160;" ::: "memory");
+#pragma unroll
+      for (int set = 0; set < 2; ++set) drain_ring(sh.full[set], stages, ci[set], sh.issued[set], kCopyWarps);
+    } else {
+      const int r = threadIdx.x - 512;
+      auto node_of = [&](const Item& q) { return r < q.count ? P.perm[q.first + r] : 0; };
+      more = next_item(&it);
+      int node = more ? node_of(it) : 0;
+      while (more) {  // (a warp that gave up keeps passing the group's barriers)
+        const Item cur = it;
+        const Entry& O = E[cur.e];
+        const int set = ni & 1;
+        int* nodes = sh.node_in[set];
+        ++ni;
+        if (r < 128) nodes[r] = (node >= 0 && node < P.N) ? node : 0;  // (a wrong node's row is not stored)
+        more = next_item(&it);
+        if (more) {
+          node = node_of(it);  // read while this tile is copied
+          if (r < 4) prefetch_nodes(P.perm, it.first + kPermAhead + 32 * r, P.N);
+        }
+        asm volatile("bar.sync 3, 160;" ::: "memory");
+        for (int s = 0; ok && s < O.count; ++s) {
+          const LinSource& Q = S[O.first + s];
+          const float* x = P.x[Q.pair] + Q.off;
+          for (int k0 = 0; k0 < Q.k; k0 += kKC) {
+            const int c = set ? ci[1]++ : ci[0]++, st = c % stages, pitch = node_pitch(O.d);
+            if (c >= stages && !wait(&sh.empty[set][st], ((c / stages) + 1) & 1, limit, abort, 5)) ok = false;
+            if (!ok) break;
+            const uint32_t dst = smem_u32(sRaw + (set * stages + st) * (kRaw / 4));
+            const int n = min(kKC, Q.k - k0) * O.d / VEC;
+            const RowShare w(n, r, kCopy);
+            for (int o = w.at; o < n; o += w.pieces) {
+              const float* src = x + k0 * O.d + o * VEC;
+              uint32_t to = dst + (w.row * pitch + o * VEC) * 4;
+              copy_rows<VEC>(src, P.dim_src, nodes, w, cur.count, to, pitch * 4);
+            }
+            copies_arrive(&sh.full[set][st]);
+          }
+        }
+      }
+      copies_wait_all();  // no copy may be in flight when the CTA ends
     }
-    copies_wait_all();  // no copy may be in flight when the CTA ends
   } else {
     // ---- MMAs: tiles of the warp's parity ----
     const int set = warp - 21;
@@ -668,9 +714,9 @@ cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStr
     }
     // shared memory: the weight, and for each pipeline an output tile and as many raw chunks (one or two) as fit
     const int fixed = 1024 + most * kWHalf + 2 * kRaw + P.n_src * int(sizeof(LinSource)) +
-                      P.n_entries * int(sizeof(Entry)) + (P.T + 2) * 4;
+                      P.n_entries * int(sizeof(Entry) + sizeof(Cut)) + (P.T + 2) * 4;
     static_assert(1024 + kMaxHalves * kWHalf + 4 * kRaw + kLinSources * int(sizeof(LinSource)) +
-                          kLinTcEntries * int(sizeof(Entry)) + (TPCONV_MAX_TYPES + 2) * 4 + int(sizeof(Shared)) + 64 <=
+                          kLinTcEntries * int(sizeof(Entry) + sizeof(Cut)) + (TPCONV_MAX_TYPES + 2) * 4 + int(sizeof(Shared)) + 64 <=
                       kSMemMax,
                   "a raw chunk always fits");
     const int stages = std::min(kMaxStages, (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / (2 * kRaw));

@@ -73,6 +73,30 @@ __device__ __forceinline__ void prefetch_nodes(const int* perm, int at, int64_t 
   if (at < N) asm volatile("prefetch.global.L2 [%0];" ::"l"(perm + at));
 }
 
+// untiled bulk copies: both addresses and the size are multiples of 16 bytes
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+// The ring's copy warps arrive on a stage's barrier with the bytes of their own bulk
+// copies.  At the end (after an abort the warps may have stopped at different chunks) the
+// arrivals that a warp left out are made up for, and the last chunks are waited for,
+// bounded: no copy is in flight when the CTA ends.  issued: the chunks of each of the
+// `warps` copy warps, written before a barrier of theirs.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int chunk, const volatile int* issued, int warps) {
+  int m = chunk;
+  for (int w = 0; w < warps; ++w) m = max(m, issued[w]);
+  if ((threadIdx.x & 31) == 0)
+    for (int c = chunk; c < m; ++c) mbar_arrive(&full[c % stages]);
+  for (int c = max(m - stages, 0); c < m; ++c)
+    if (!mbar_wait_for(&full[c % stages], (c / stages) & 1, kDrainLimitNs)) break;
+}
+
 // How `threads` threads share rows of `n` pieces: as many whole rows at a time as
 // fit (or, for longer rows, the pieces of one row in turn); a thread keeps its place
 // in the row, so that a step costs an addition and not a division.
@@ -188,6 +212,76 @@ __device__ __forceinline__ int64_t div_cost(int64_t a, int b) {
 __device__ __forceinline__ int64_t share_begin(int64_t total, int b, int shares) {
   const int64_t q = div_cost(total, shares);
   return q * b + min(int64_t(b), total - q * shares);
+}
+
+// ---- a CTA's share of a list of work ----------------------------------------------
+// Entries in order, in each the units (tiles or chunks of `nodes` consecutive nodes) of
+// the types; share b owns the units whose cost begins in it, and meets them as runs:
+// nodes [first, end) of one type in one entry.  Every warp walks the same list by
+// itself; where it stands between two runs is kept in shared memory (a register copy in
+// every role cost more than the walk: 600 cycles a tile), and next_run is one function.
+struct Cut {
+  int cost, nodes, which;  // of a unit; which: index of the unit kind's total
+};
+struct Run {
+  int e, t, first, end;  // e < 0: no more
+};
+struct WalkState {
+  int64_t base, lo, hi;  // cost before the entry, the share's costs
+  int left, e, t, at;    // units of the share left in the entry, entry, type, next node
+};
+__device__ __forceinline__ void walk_begin(WalkState* w, int64_t total) {
+  if ((threadIdx.x & 31) == 0) {
+    w->base = 0;
+    w->lo = share_begin(total, blockIdx.x, gridDim.x);
+    w->hi = share_begin(total, blockIdx.x + 1, gridDim.x);
+    w->left = 0, w->e = -1, w->t = 0, w->at = 0;
+  }
+  __syncwarp();
+}
+static __device__ __noinline__ Run next_run(WalkState* w, const Cut* cuts, int n_cuts, const int* total,
+                                            const int* offs, int T) {
+  WalkState s = *w;
+  __syncwarp();
+  if (s.e >= n_cuts) return {-1, 0, 0, 0};
+  if (s.left == 0) {
+    for (;;) {
+      if (s.e >= 0) s.base += int64_t(total[cuts[s.e].which]) * cuts[s.e].cost;
+      if (++s.e >= n_cuts || s.base >= s.hi) {
+        if ((threadIdx.x & 31) == 0) w->e = n_cuts, w->left = 0, w->base = s.hi;
+        __syncwarp();
+        return {-1, 0, 0, 0};
+      }
+      const int c = cuts[s.e].cost;
+      const int64_t n = total[cuts[s.e].which];
+      const int64_t a = s.lo <= s.base ? 0 : min(div_cost(s.lo - s.base + c - 1, c), n),
+                    b = min(div_cost(s.hi - s.base + c - 1, c), n);
+      if (a < b) {
+        s.left = int(b - a);
+        int j;
+        seek_unit(offs, T, cuts[s.e].nodes, a, &s.t, &j);
+        s.at = s.t < T ? offs[s.t] + j * cuts[s.e].nodes : 0;
+        break;
+      }
+    }
+  } else {
+    ++s.t;
+    s.at = s.t < T ? offs[s.t] : 0;
+  }
+  const int nodes = cuts[s.e].nodes;
+  while (s.t < T && s.at >= offs[s.t + 1]) {
+    ++s.t;
+    s.at = s.t < T ? offs[s.t] : 0;
+  }
+  Run r{-1, 0, 0, 0};
+  if (s.t < T) {
+    const int end = offs[s.t + 1], take = min((end - s.at + nodes - 1) / nodes, s.left);
+    r = {s.e, s.t, s.at, end - s.at <= take * nodes ? end : s.at + take * nodes};
+    s.left -= take;
+  }
+  if ((threadIdx.x & 31) == 0) *w = s;
+  __syncwarp();
+  return r;
 }
 
 }  // namespace tc
