@@ -5,9 +5,9 @@
 //
 // per path, 128 input channels and 64 output channels: a product whose depth is the
 // ragged row count of the type.  A chunk is the rows of 64, 21, 12 or 9 nodes
-// (l = 0..3: 64, 63, 60, 63 rows, filled up with zeros); copy threads gather the nodes'
-// pieces of x and g by perm, 16 bytes a thread (4 where a block or tensor is not aligned
-// for it).  The A operand is x transposed: thread u reads its channel of every row (the
+// (l = 0..3: 64, 63, 60, 63 rows, filled up with zeros); copy warps gather the nodes'
+// pieces of x and g by perm, a bulk copy each (4-byte asynchronous copies where a block
+// or tensor is not 16-byte aligned).  The A operand is x transposed: thread u reads its channel of every row (the
 // lanes of a warp are 2l+1 floats apart: no bank conflicts), splits it (3xTF32) and
 // stores hi and lo to TMEM, lane = u, column = row.  The B operand is g: thread w
 // reads its channel and writes hi and lo into the K-major 128-byte-swizzled tile, lo
@@ -26,7 +26,7 @@
 // is 512 B from HBM and about 2.3 KB of shared-memory traffic.
 // Two sets of warps convert every second chunk each (the latency of a chunk's steps is
 // what bounds it): warps 0-3 and 8-11 x, 4-7 and 12-15 g; 16-23 add finished banks (32
-// columns each) and store, 24-26 copy, 27 issues the MMAs.  Waits are bounded as in the
+// columns each) and store, 24-29 copy, 30 issues the MMAs.  Waits are bounded as in the
 // row kernel.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -52,8 +52,8 @@ constexpr int kBHalf = 2 * kNT * 128;         // 32 rows of B: 64 columns' hi an
 constexpr int kBTile = 2 * kBHalf;
 constexpr int kMaxStages = 4;                 // raw chunks, an even number
 constexpr int kSMemMax = 227 * 1024;
-constexpr int kThreads = 896;
-constexpr int kCopy = 96;                     // copy threads
+constexpr int kThreads = 992;
+constexpr int kCopyWarps = 6, kCopy = 32 * kCopyWarps;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemA = 0, kTmemAStage = 2 * kKMax, kTmemD = 256, kTmemDStage = 128;  // A: hi | lo, D: D1 | D2
 
@@ -62,10 +62,10 @@ __host__ __device__ constexpr int chunk_nodes(int d) { return kKMax / d; }
 
 // (path, 128 input channels, 64 output channels)
 struct Entry {
-  int d, cost;      // 2l+1; cost of a chunk
+  int d;            // 2l+1
   int xoff, goff;   // first columns in x and g
   int cu, cw;       // channels
-  int co, pad;      // output channels of the path: the pitch of its weight
+  int co;           // output channels of the path: the pitch of its weight
   int64_t woff;     // first weight
 };
 struct Params {
@@ -76,6 +76,7 @@ struct Params {
   const int *perm, *offsets;
   int coef[4];  // cost of a chunk of d = 1, 3, 5, 7, summed over the entries
   Entry e[kLinGradTcEntries];
+  Cut cut[kLinGradTcEntries];
 };
 
 struct Shared {
@@ -84,17 +85,19 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int total[4];  // chunks of all types for d = 1, 3, 5, 7
+  WalkState walk[kThreads / 32];
   int node[2][64];
+  int issued[kCopyWarps];
 };
 
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, uint64_t limit, volatile int* abort, int code) {
   return wait_or_abort(b, parity, limit, abort, &g_linear_grad_error, code);
 }
 
-__device__ __forceinline__ int64_t total_cost(const Params& P, const int* total) {
-  int64_t c = 0;
+__device__ __forceinline__ int total_cost(const Params& P, const int* total) {
+  int c = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c += int64_t(total[i]) * P.coef[i];
+  for (int i = 0; i < 4; ++i) c += total[i] * P.coef[i];
   return c;
 }
 
@@ -104,53 +107,18 @@ struct Piece {
   int slot;  // partial tile, or -1: the type's rows are all here
 };
 
-// CTA b owns the chunks whose cost begins in its share.  Every warp walks the same list.
 struct Walk {
-  const Entry* E;
-  const int* offs;
-  const int* total;
-  int n_entries, T;
-  int64_t lo, hi, base = 0, left = 0;
-  int e = -1, unit = 1, t = 0, j = 0, n = 0;
+  WalkState* w;
+  const Cut* cuts;
+  const int *total, *offs;
+  int n, T;
 
-  __device__ Walk(const Params& P, const Entry* entries, const int* o, const int* tot)
-      : E(entries), offs(o), total(tot), n_entries(P.n_entries), T(P.T) {
-    const int64_t c = total_cost(P, tot);
-    lo = share_begin(c, blockIdx.x, gridDim.x);
-    hi = share_begin(c, blockIdx.x + 1, gridDim.x);
-  }
-  __device__ bool next(Piece* q) {
-    if (left == 0) {
-      for (;;) {
-        if (e >= 0) base += int64_t(total[E[e].d >> 1]) * E[e].cost;
-        if (++e >= n_entries || base >= hi) {
-          e = n_entries;
-          return false;
-        }
-        const int c = E[e].cost;
-        const int64_t all = total[E[e].d >> 1];
-        const int64_t a = lo <= base ? 0 : min(div_cost(lo - base + c - 1, c), all),
-                      b = min(div_cost(hi - base + c - 1, c), all);
-        if (a < b) {
-          left = b - a;
-          unit = chunk_nodes(E[e].d);
-          seek_unit(offs, T, unit, a, &t, &j);
-          n = t < T ? group_units(offs, t, unit) : 0;
-          break;
-        }
-      }
-    }
-    while (j >= n) {
-      if (t + 1 >= T) return false;
-      ++t, j = 0;
-      n = group_units(offs, t, unit);
-    }
-    const int c = int(min(int64_t(n - j), left));
-    q->e = e, q->t = t;
-    q->first = offs[t] + j * unit;
-    q->nodes = min(offs[t + 1] - q->first, c * unit);
-    q->slot = (j == 0 && c == n) ? -1 : 2 * int(blockIdx.x) + (j == 0);
-    j += c, left -= c;
+  __device__ __forceinline__ bool next(Piece* q) {
+    const Run r = next_run(w, cuts, n, total, offs, T);
+    if (r.e < 0) return false;
+    const bool begins = r.first == offs[r.t], ends = r.end == offs[r.t + 1];
+    q->e = r.e, q->t = r.t, q->first = r.first, q->nodes = r.end - r.first;
+    q->slot = begins && ends ? -1 : 2 * int(blockIdx.x) + begins;
     return true;
   }
 };
@@ -235,17 +203,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* sB = base;  // of each set
   unsigned char* sRaw = base + 2 * kBTile;
   Entry* E = reinterpret_cast<Entry*>(sRaw + stages * stage_bytes);
-  int* offs = reinterpret_cast<int*>(E + P.n_entries);
+  Cut* cuts = reinterpret_cast<Cut*>(E + P.n_entries);
+  int* offs = reinterpret_cast<int*>(cuts + P.n_entries);
   __shared__ Shared sh;
   volatile int* abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   for (int i = threadIdx.x; i < P.n_entries * int(sizeof(Entry) / 4); i += kThreads)
     reinterpret_cast<int*>(E)[i] = reinterpret_cast<const int*>(P.e)[i];
+  for (int i = threadIdx.x; i < P.n_entries * int(sizeof(Cut) / 4); i += kThreads)
+    reinterpret_cast<int*>(cuts)[i] = reinterpret_cast<const int*>(P.cut)[i];
   load_offsets(offs, P.offsets, P.T, P.N);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&sh.full[s], kCopy);
+      mbar_init(&sh.full[s], VEC == 4 ? kCopyWarps : kCopy);
       mbar_init(&sh.empty[s], 256);
     }
     for (int i = 0; i < 2; ++i) {
@@ -258,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 27) tmem_alloc(&sh.tmem, kTmemCols);
+  if (warp == 30) tmem_alloc(&sh.tmem, kTmemCols);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
@@ -269,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  Walk walk(P, E, offs, sh.total);
+  walk_begin(&sh.walk[warp], total_cost(P, sh.total));
+  Walk walk{&sh.walk[warp], cuts, sh.total, offs, P.n_entries, P.T};
   Piece q;
   bool ok = true;
   int ci = 0;  // chunks so far
@@ -372,37 +344,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < 27) {
+  } else if (warp < 30) {
     // ---- node rows to shared memory, several chunks ahead ----
     const int r = threadIdx.x - 768;
-    while (walk.next(&q)) {  // (a warp that gave up keeps passing the group's barriers)
-      const Entry& L = E[q.e];
-      const int d = L.d, nq = chunk_nodes(d), lx = L.cu * d, lg = L.cw * d;
-      const float *x = P.x + L.xoff, *g = P.g + L.goff;
-      // the nodes of the next chunk are read while this one is copied
-      int node = r < min(nq, q.nodes) ? P.perm[q.first + r] : 0;
-      for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-        const int st = ci % stages, cnt = min(nq, q.nodes - n0);
-        int* nodes = sh.node[ci & 1];
-        if (r < 64) nodes[r] = (node >= 0 && node < P.N) ? node : 0;
-        asm volatile("bar.sync 1, 96;" ::: "memory");
-        node = r < nq && n0 + nq + r < q.nodes ? P.perm[q.first + n0 + nq + r] : 0;
-        if (r < 2) prefetch_nodes(P.perm, q.first + n0 + kPermAhead + 32 * r, P.N);
-        if (ok && ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
-        if (!ok) continue;
-        const uint32_t dst = smem_u32(sRaw + st * stage_bytes);
-        auto rows = [&](const float* src, int dim, int len, uint32_t to0) {
-          const int n = len / VEC;
-          const RowShare w(n, r, kCopy);
-          for (int o = w.at; o < n; o += w.pieces)
-            copy_rows<VEC>(src + o * VEC, dim, nodes, w, cnt, to0 + (w.row * len + o * VEC) * 4, len * 4);
+    if constexpr (VEC == 4) {
+      // a bulk copy per node and tensor, dealt out over the warps (issuing one takes some
+      // 60 cycles): copy i of a chunk is node i / 2 of x or g
+      static_assert(kCopy >= 2 * kKMax, "a copy a thread");
+      const int w = warp - 24, i0 = lane * kCopyWarps + w;
+      while (ok && walk.next(&q)) {
+        const Entry& L = E[q.e];
+        const int d = L.d, nq = chunk_nodes(d), lx = L.cu * d, lg = L.cw * d;
+        const bool is_g = i0 & 1;
+        const float* src = is_g ? P.g + L.goff : P.x + L.xoff;
+        const int dim = is_g ? P.dim_g : P.dim_x;
+        const uint32_t bytes = uint32_t(is_g ? lg : lx) * 4;
+        auto node_of = [&](int k) {
+          const int n = k < q.nodes ? P.perm[q.first + k] : 0;
+          return n >= 0 && n < P.N ? n : 0;
         };
-        rows(x, P.dim_x, lx, dst);
-        rows(g, P.dim_g, lg, dst + g_offset);
-        copies_arrive(&sh.full[st]);
+        const int k = i0 / 2;
+        int node = k < nq ? node_of(k) : 0;  // of the next chunk, read while this one is copied
+        for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
+          const int st = ci % stages, cnt = min(nq, q.nodes - n0);
+          const float* from = src + int64_t(node) * dim;
+          if (k < nq && n0 + nq < q.nodes) node = node_of(n0 + nq + k);
+          if (r < 2) prefetch_nodes(P.perm, q.first + n0 + kPermAhead + 32 * r, P.N);
+          const uint32_t mine = __reduce_add_sync(0xffffffffu, k < cnt ? bytes : 0u);
+          if (ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(&sh.full[st], mine);
+          __syncwarp();
+          if (k < cnt)
+            bulk_load(smem_u32(sRaw + st * stage_bytes) + (is_g ? g_offset : 0) + k * bytes, from, bytes, &sh.full[st]);
+        }
       }
+      if (lane == 0) sh.issued[w] = ci;
+      asm volatile("bar.sync 1, 192;" ::: "memory");
+      drain_ring(sh.full, stages, ci, sh.issued, kCopyWarps);
+    } else {
+      while (walk.next(&q)) {  // (a warp that gave up keeps passing the group's barriers)
+        const Entry& L = E[q.e];
+        const int d = L.d, nq = chunk_nodes(d), lx = L.cu * d, lg = L.cw * d;
+        const float *x = P.x + L.xoff, *g = P.g + L.goff;
+        // the nodes of the next chunk are read while this one is copied
+        int node = r < min(nq, q.nodes) ? P.perm[q.first + r] : 0;
+        for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
+          const int st = ci % stages, cnt = min(nq, q.nodes - n0);
+          int* nodes = sh.node[ci & 1];
+          if (r < 64) nodes[r] = (node >= 0 && node < P.N) ? node : 0;
+          asm volatile("bar.sync 1, 192;" ::: "memory");
+          node = r < nq && n0 + nq + r < q.nodes ? P.perm[q.first + n0 + nq + r] : 0;
+          if (r < 2) prefetch_nodes(P.perm, q.first + n0 + kPermAhead + 32 * r, P.N);
+          if (ok && ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
+          if (!ok) continue;
+          const uint32_t dst = smem_u32(sRaw + st * stage_bytes);
+          auto rows = [&](const float* src, int dim, int len, uint32_t to0) {
+            const int n = len / VEC;
+            const RowShare w(n, r, kCopy);
+            for (int o = w.at; o < n; o += w.pieces)
+              copy_rows<VEC>(src + o * VEC, dim, nodes, w, cnt, to0 + (w.row * len + o * VEC) * 4, len * 4);
+          };
+          rows(x, P.dim_x, lx, dst);
+          rows(g, P.dim_g, lg, dst + g_offset);
+          copies_arrive(&sh.full[st]);
+        }
+      }
+      copies_wait_all();  // no copy may be in flight when the CTA ends
     }
-    copies_wait_all();  // no copy may be in flight when the CTA ends
   } else {
     // ---- MMAs ----
     int ri = 0;
@@ -444,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before_sync();
   __syncthreads();
-  if (warp == 27) {
+  if (warp == 30) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -472,28 +481,26 @@ __global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant_
   if (r0 >= r1) return;
   if (warp == 0) {
     // the slots of the type's pieces
-    const int unit = chunk_nodes(L.d), n = group_units(offs, t, unit), c = L.cost;
+    const int unit = chunk_nodes(L.d), n = group_units(offs, t, unit), c = P.cut[e].cost;
     int m = -1;
     if (n == 0) {
       m = 0;
     } else {
-      const int64_t all = total_cost(P, total);
-      int64_t seg = int64_t(count_units(offs, t, unit)) * c;  // cost before the type's first chunk
-      for (int k = 0; k < e; ++k) seg += int64_t(total[P.e[k].d >> 1]) * P.e[k].cost;
-      const int64_t end = seg + int64_t(n - 1) * c;  // cost before its last chunk
+      const int all = total_cost(P, total);
+      int seg = count_units(offs, t, unit) * c;  // cost before the type's first chunk
+      for (int k = 0; k < e; ++k) seg += total[P.cut[k].which] * P.cut[k].cost;
+      const int end = seg + (n - 1) * c;  // cost before its last chunk
       // the shares that hold the first and the last chunk
-      const int64_t per = div_cost(all, ctas), more = all - per * ctas, wide = more * (per + 1);
-      auto owner = [&](int64_t x) {
-        return x < wide ? int(div_cost(x, int(per + 1))) : int(more + div_cost(x - wide, int(max(per, int64_t(1)))));
-      };
+      const int per = all / ctas, more = all - per * ctas, wide = more * (per + 1);
+      auto owner = [&](int x) { return x < wide ? x / (per + 1) : more + (x - wide) / max(per, 1); };
       const int first = owner(seg), last = owner(end);
       m = 0;
       for (int b0 = first; b0 <= last; b0 += 32) {
         const int b = b0 + threadIdx.x;
         bool has = b == first;
         if (b > first && b <= last) {  // a share narrower than a chunk's cost may hold none
-          const int64_t lo = per * b + min(int64_t(b), more), hi = per * (b + 1) + min(int64_t(b + 1), more);
-          has = seg + div_cost(lo - seg + c - 1, c) * c < hi;
+          const int lo = per * b + min(b, more), hi = per * (b + 1) + min(b + 1, more);
+          has = seg + (lo - seg + c - 1) / c * c < hi;
         }
         const unsigned mask = __ballot_sync(0xffffffffu, has);
         if (has) slot[m + __popc(mask & ((1u << threadIdx.x) - 1))] = 2 * b + (b == first);
@@ -571,15 +578,19 @@ cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t l
         E.cu = std::min(kMT, L.ci - u0), E.cw = std::min(kNT, L.co - w0), E.co = L.co;
         E.woff = L.woff + int64_t(u0) * L.co + w0;
         // the KB that a chunk moves, and what any chunk takes
-        E.cost = 16 + (E.cu + E.cw) * L.d * chunk_nodes(L.d) / 256;
-        P.coef[L.d >> 1] += E.cost;
+        P.cut[P.n_entries - 1] = {16 + (E.cu + E.cw) * L.d * chunk_nodes(L.d) / 256, chunk_nodes(L.d), L.d >> 1};
         sx = std::max(sx, E.cu * L.d * chunk_nodes(L.d) * 4);
         sg = std::max(sg, E.cw * L.d * chunk_nodes(L.d) * 4);
       }
   }
+  const int shift = cost_shift(P.cut, P.n_entries, G.N, G.T);
+  for (int i = 0; i < P.n_entries; ++i) {
+    P.cut[i].cost = std::max(1, P.cut[i].cost >> shift);
+    P.coef[P.cut[i].which] += P.cut[i].cost;
+  }
   sx = (sx + 15) & ~15;
   const int stage = (sx + sg + 15) & ~15;
-  const int fixed = 1024 + 2 * kBTile + P.n_entries * int(sizeof(Entry)) + (P.T + 2) * 4;
+  const int fixed = 1024 + 2 * kBTile + P.n_entries * int(sizeof(Entry) + sizeof(Cut)) + (P.T + 2) * 4;
   // at most 32 KB of x and 16 KB of g: two stages always fit; an even number, so that a stage
   // belongs to one set of converters
   const int stages = std::min(kMaxStages, (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / stage) & ~1;

@@ -82,12 +82,13 @@ constexpr int col_tiles(int n) { return (n + kNT - 1) / kNT; }
 
 // (output block, 64 columns)
 struct Entry {
-  int d, cost;       // 2l+1; cost of a tile: its chunks plus one
+  int d;             // 2l+1
   int off, nw;       // first output column, channels
   int c0;            // first channel of the block
   int first, count;  // sources
   int pad;
 };
+static_assert(sizeof(Entry) % 4 == 0 && sizeof(Cut) % 4 == 0 && sizeof(LinSource) % 8 == 0, "copied by words");
 struct Params {
   int n_entries, n_src, T, dim_src, dim_out;
   int64_t N, wnumel;
@@ -97,6 +98,7 @@ struct Params {
   int coef[4];     // cost of a tile of d = 1, 3, 5, 7, summed over the entries
   int accumulate;  // add to the output (and leave the rows without a type alone)
   Entry e[kLinTcEntries];
+  Cut cut[kLinTcEntries];  // cost of a tile: its chunks plus one
   LinSource s[kLinSources];
 };
 
@@ -240,10 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     reinterpret_cast<int*>(S)[i] = reinterpret_cast<const int*>(P.s)[i];
   for (int i = threadIdx.x; i < P.n_entries * int(sizeof(Entry) / 4); i += kThreads)
     reinterpret_cast<int*>(E)[i] = reinterpret_cast<const int*>(P.e)[i];
-  if (threadIdx.x < P.n_entries) {
-    const int d = P.e[threadIdx.x].d;
-    cuts[threadIdx.x] = {P.e[threadIdx.x].cost, tile_of(d), d >> 1};
-  }
+  for (int i = threadIdx.x; i < P.n_entries * int(sizeof(Cut) / 4); i += kThreads)
+    reinterpret_cast<int*>(cuts)[i] = reinterpret_cast<const int*>(P.cut)[i];
   load_offsets(offs, P.offsets, P.T, P.N);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -274,9 +274,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   {
-    int64_t c = 0;
+    int c = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c += int64_t(sh.total[i]) * P.coef[i];
+    for (int i = 0; i < 4; ++i) c += sh.total[i] * P.coef[i];
     walk_begin(&sh.walk[warp], c);
   }
   Walk walk{&sh.walk[warp], E, cuts, sh.total, offs, P.n_entries, P.T};
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this CTA's share of the nodes without a type: zero rows, a warp each
     if (!P.accumulate) {
       const int b = offs[P.T], nz = max(int(P.N) - b, 0);
-      const int z0 = b + int(share_begin(nz, blockIdx.x, gridDim.x)), z1 = b + int(share_begin(nz, blockIdx.x + 1, gridDim.x));
+      const int z0 = b + share_begin(nz, blockIdx.x, gridDim.x), z1 = b + share_begin(nz, blockIdx.x + 1, gridDim.x);
       for (int i = z0 + (warp - 8); i < z1; i += 8) {
         const int n = P.perm[i];
         if (n < 0 || n >= P.N) continue;
@@ -707,10 +707,15 @@ cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStr
       if (pass > 0 && chunks == 0) continue;
       most = std::max(most, halves);
       for (int c0 = 0; c0 < O.n; c0 += kNT) {
-        P.e[P.n_entries++] = {O.d, chunks + 1, O.off + c0 * O.d, std::min(kNT, O.n - c0), c0, first, P.n_src - first, 0};
-        P.coef[O.d >> 1] += chunks + 1;
+        P.cut[P.n_entries] = {chunks + 1, tile_of(O.d), O.d >> 1};
+        P.e[P.n_entries++] = {O.d, O.off + c0 * O.d, std::min(kNT, O.n - c0), c0, first, P.n_src - first, 0};
       }
       tiles += (R.N / tile_of(O.d) + std::min<int64_t>(R.T, R.N)) * col_tiles(O.n);
+    }
+    const int shift = cost_shift(P.cut, P.n_entries, R.N, R.T);
+    for (int i = 0; i < P.n_entries; ++i) {
+      P.cut[i].cost = std::max(1, P.cut[i].cost >> shift);
+      P.coef[P.cut[i].which] += P.cut[i].cost;
     }
     // shared memory: the weight, and for each pipeline an output tile and as many raw chunks (one or two) as fit
     const int fixed = 1024 + most * kWHalf + 2 * kRaw + P.n_src * int(sizeof(LinSource)) +

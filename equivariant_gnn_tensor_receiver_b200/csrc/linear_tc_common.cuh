@@ -180,9 +180,9 @@ __device__ __forceinline__ int count_units(const int* offs, int groups, int unit
   return __reduce_add_sync(0xffffffffu, s);
 }
 // the group of unit `at`, and its index there
-__device__ __forceinline__ void seek_unit(const int* offs, int groups, int unit, int64_t at, int* t, int* j) {
+__device__ __forceinline__ void seek_unit(const int* offs, int groups, int unit, int at, int* t, int* j) {
   const int lane = threadIdx.x & 31;
-  int64_t carry = 0;
+  int carry = 0;
   *t = groups, *j = 0;
   for (int t0 = 0; t0 < groups; t0 += 32) {
     const int n = t0 + lane < groups ? group_units(offs, t0 + lane, unit) : 0;
@@ -192,26 +192,24 @@ __device__ __forceinline__ void seek_unit(const int* offs, int groups, int unit,
       const int u = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += u;
     }
-    const int64_t first = carry + s - n;
+    const int first = carry + s - n;
     const unsigned hit = __ballot_sync(0xffffffffu, at >= first && at < first + n);
     if (hit) {
       const int src = __ffs(hit) - 1;
       *t = t0 + src;
-      *j = int(at - __shfl_sync(0xffffffffu, first, src));
+      *j = at - __shfl_sync(0xffffffffu, first, src);
       return;
     }
     carry += __shfl_sync(0xffffffffu, s, 31);
   }
 }
 
-// non-negative division; 32-bit where the operands fit
-__device__ __forceinline__ int64_t div_cost(int64_t a, int b) {
-  return a <= 0xffffffffll ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
-}
-// the first cost of share b of `shares` equal ones
-__device__ __forceinline__ int64_t share_begin(int64_t total, int b, int shares) {
-  const int64_t q = div_cost(total, shares);
-  return q * b + min(int64_t(b), total - q * shares);
+// The first cost of share b of `shares` equal ones.  Costs are 32-bit (the host scales
+// them to a total below 2^31): the walks are short, and 64-bit divisions made them the
+// longest part of a small call.
+__device__ __forceinline__ int share_begin(int total, int b, int shares) {
+  const int q = total / shares;
+  return q * b + min(b, total - q * shares);
 }
 
 // ---- a CTA's share of a list of work ----------------------------------------------
@@ -227,10 +225,10 @@ struct Run {
   int e, t, first, end;  // e < 0: no more
 };
 struct WalkState {
-  int64_t base, lo, hi;  // cost before the entry, the share's costs
-  int left, e, t, at;    // units of the share left in the entry, entry, type, next node
+  int base, lo, hi;    // cost before the entry, the share's costs
+  int left, e, t, at;  // units of the share left in the entry, entry, type, next node
 };
-__device__ __forceinline__ void walk_begin(WalkState* w, int64_t total) {
+__device__ __forceinline__ void walk_begin(WalkState* w, int total) {
   if ((threadIdx.x & 31) == 0) {
     w->base = 0;
     w->lo = share_begin(total, blockIdx.x, gridDim.x);
@@ -246,18 +244,17 @@ static __device__ __noinline__ Run next_run(WalkState* w, const Cut* cuts, int n
   if (s.e >= n_cuts) return {-1, 0, 0, 0};
   if (s.left == 0) {
     for (;;) {
-      if (s.e >= 0) s.base += int64_t(total[cuts[s.e].which]) * cuts[s.e].cost;
+      if (s.e >= 0) s.base += total[cuts[s.e].which] * cuts[s.e].cost;
       if (++s.e >= n_cuts || s.base >= s.hi) {
         if ((threadIdx.x & 31) == 0) w->e = n_cuts, w->left = 0, w->base = s.hi;
         __syncwarp();
         return {-1, 0, 0, 0};
       }
       const int c = cuts[s.e].cost;
-      const int64_t n = total[cuts[s.e].which];
-      const int64_t a = s.lo <= s.base ? 0 : min(div_cost(s.lo - s.base + c - 1, c), n),
-                    b = min(div_cost(s.hi - s.base + c - 1, c), n);
+      const int n = total[cuts[s.e].which];
+      const int a = s.lo <= s.base ? 0 : min((s.lo - s.base + c - 1) / c, n), b = min((s.hi - s.base + c - 1) / c, n);
       if (a < b) {
-        s.left = int(b - a);
+        s.left = b - a;
         int j;
         seek_unit(offs, T, cuts[s.e].nodes, a, &s.t, &j);
         s.at = s.t < T ? offs[s.t] + j * cuts[s.e].nodes : 0;
@@ -282,6 +279,16 @@ static __device__ __noinline__ Run next_run(WalkState* w, const Cut* cuts, int n
   if ((threadIdx.x & 31) == 0) *w = s;
   __syncwarp();
   return r;
+}
+
+// how far the costs of a list are to be shifted down (to 1 at least) for a total below 2^31
+inline int cost_shift(const Cut* cuts, int n, int64_t nodes, int T) {
+  for (int s = 0;; ++s) {
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i)
+      total += (nodes / cuts[i].nodes + T) * (cuts[i].cost >> s > 1 ? cuts[i].cost >> s : 1);
+    if (total < (int64_t(1) << 31) - (1 << 20) || s == 31) return s;
+  }
 }
 
 }  // namespace tc
