@@ -577,8 +577,11 @@ cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t l
         E.d = L.d, E.xoff = L.xoff + u0 * L.d, E.goff = L.goff + w0 * L.d;
         E.cu = std::min(kMT, L.ci - u0), E.cw = std::min(kNT, L.co - w0), E.co = L.co;
         E.woff = L.woff + int64_t(u0) * L.co + w0;
-        // the KB that a chunk moves, and what any chunk takes
-        P.cut[P.n_entries - 1] = {16 + (E.cu + E.cw) * L.d * chunk_nodes(L.d) / 256, chunk_nodes(L.d), L.d >> 1};
+        // the KB that a chunk moves, what any chunk takes, and more where the copies of a
+        // chunk take long to issue (l = 0: 1.4 times the others)
+        P.cut[P.n_entries - 1] = {16 + (E.cu + E.cw) * L.d * chunk_nodes(L.d) / 256 +
+                                      std::max(0, 2 * chunk_nodes(L.d) - 40) / 4,
+                                  chunk_nodes(L.d), L.d >> 1};
         sx = std::max(sx, E.cu * L.d * chunk_nodes(L.d) * 4);
         sg = std::max(sg, E.cw * L.d * chunk_nodes(L.d) * 4);
       }

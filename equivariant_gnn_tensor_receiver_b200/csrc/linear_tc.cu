@@ -98,7 +98,7 @@ struct Params {
   int coef[4];     // cost of a tile of d = 1, 3, 5, 7, summed over the entries
   int accumulate;  // add to the output (and leave the rows without a type alone)
   Entry e[kLinTcEntries];
-  Cut cut[kLinTcEntries];  // cost of a tile: its chunks plus one
+  Cut cut[kLinTcEntries];  // cost of a tile: by its chunks
   LinSource s[kLinSources];
 };
 
@@ -707,7 +707,8 @@ cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStr
       if (pass > 0 && chunks == 0) continue;
       most = std::max(most, halves);
       for (int c0 = 0; c0 < O.n; c0 += kNT) {
-        P.cut[P.n_entries] = {chunks + 1, tile_of(O.d), O.d >> 1};
+        // (measured, l = 0..2: 1.2, 1.05 and 1 times: the more nodes, the more copies to issue)
+        P.cut[P.n_entries] = {10 * (chunks + 1) + chunks * tile_of(O.d) / 30, tile_of(O.d), O.d >> 1};
         P.e[P.n_entries++] = {O.d, O.off + c0 * O.d, std::min(kNT, O.n - c0), c0, first, P.n_src - first, 0};
       }
       tiles += (R.N / tile_of(O.d) + std::min<int64_t>(R.T, R.N)) * col_tiles(O.n);
