@@ -252,7 +252,7 @@ int grad_unit(const tpconv_linear* p, int64_t N) {
     cw = std::max(cw, ceil_div(p->path[i].co, kTC));
   }
   const int64_t want = std::max<int64_t>(1, 2 * kSMs / std::max(1, p->n_paths * cu * cw));
-  return int(std::max<int64_t>(64, (N + want - 1) / want));
+  return int(std::max<int64_t>(16, (N + want - 1) / want));
 }
 size_t grad_partials(const tpconv_linear* p, int64_t N) {
   if (N == 0 || p->wnumel == 0) return 0;
@@ -289,8 +289,27 @@ void fill_rows(const tpconv_linear* p, bool transposed, int pairs, LinRows* R) {
   }
 }
 
+// multiply-adds of one pass over all paths, in millions
+double mega_macs(const tpconv_linear* p, int64_t N) {
+  double m = 0;
+  for (int i = 0; i < p->n_paths; ++i) m += double(p->path[i].ci) * p->path[i].co * p->path[i].d;
+  return m * 1e-6 * double(N);
+}
+
+// Small products run on the FP32 pipes whatever the mode (and are no less exact): the
+// tensor-core kernel takes 8 to 9 us before its first tile is stored.  Measured, FP32 /
+// tensor cores in us: 8 channels, 64 to 4096 nodes 8.3 / 12.4; 32 channels, 512 nodes
+// 10.3 / 12.4, 1024 nodes 13 / 12.4; 64 channels, 32 nodes 18.4 / 12.3 (its depth is
+// walked 16 channels a step).
 cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph, cudaStream_t st) {
-  const int tc = p->gemm != TPCONV_GEMM_SIMT ? linear_tc_launches(R) : 0;
+  int depth = 0;  // most channels that an output block sums over
+  for (int b = 0; b < R.n_out; ++b) {
+    int k = 0;
+    for (int s = 0; s < R.o[b].count; ++s) k += R.s[R.o[b].first + s].k;
+    depth = std::max(depth, k);
+  }
+  const bool small = depth <= 32 && mega_macs(p, R.N) <= 5;
+  const int tc = p->gemm != TPCONV_GEMM_SIMT && !small ? linear_tc_launches(R) : 0;
   if (tc > 0) {
     ph.note(tc);
     return linear_tc_rows(R, p->gemm == TPCONV_GEMM_FP32, device_wait_limit(), st);
@@ -307,6 +326,9 @@ cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph
   return cudaGetLastError();
 }
 
+// As for the rows, small calls run on the FP32 pipes.  Measured, FP32 / tensor cores in us:
+// 64x0e+64x1o+64x2e, 64 nodes 14.4 / 16.5, 512 nodes 18.5 / 19.1 (8 types) and 18.5 / 22.6
+// (one); 128 channels up to l = 3, 32 nodes 16.5 / 18.5, 512 nodes 43 / 27.
 cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, const int* offsets, const float* x,
                             const float* g, float* dw, float* part, NodePhase& ph, cudaStream_t st) {
   if (p->wnumel == 0) return cudaSuccess;
@@ -316,7 +338,8 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
   G.dim_x = p->dim_in, G.dim_g = p->dim_out;
   G.x = x, G.g = g, G.dw = dw, G.perm = perm, G.offsets = offsets;
   std::copy(p->path, p->path + p->n_paths, G.p);
-  if (p->gemm != TPCONV_GEMM_SIMT && linear_grad_tc_supported(G)) {
+  const bool small = N <= 512 && mega_macs(p, N) <= 20;
+  if (p->gemm != TPCONV_GEMM_SIMT && !small && linear_grad_tc_supported(G)) {
     ph.note(2);
     return linear_grad_tc(G, p->gemm == TPCONV_GEMM_FP32, part, device_wait_limit(), st);
   }

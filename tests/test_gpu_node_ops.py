@@ -190,7 +190,12 @@ LINEARS = [
     ("32x0e+16x1o", "32x0e+16x1o", 0, 3), ("64x1o", "64x1o", 1, 5), ("96x0e+64x0e", "72x0e", 333, 4),
     ("200x0e+4x0e", "64x0e", 140, 2), ("64x0e+64x1o+64x2e", "64x0e+64x1o+64x2e", 4096, 10),
     ("32x0e+32x1o", "64x0e+32x1o", 2500, 60), ("128x0e+128x1o+128x2e", "96x0e+130x1o+8x2e", 1500, 9),
-    ("20x0e+20x0e+20x0e+20x0e+20x0e+300x1o", "16x0e+8x1o", 900, 31)]
+    ("20x0e+20x0e+20x0e+20x0e+20x0e+300x1o", "16x0e+8x1o", 900, 31),
+    # small channels with enough rows for the tensor cores, and odd ones of every kind
+    ("16x0e+5x1o+1x3o", "12x0e+7x1o+3x3o", 30_000, 3), ("37x0e+21x1o+5x2e", "50x0e+19x1o+7x2e", 1101, 7),
+    ("16x3o+12x2e", "20x3o+8x2e", 12_345, 256), ("1x0e", "1x0e", 700, 2), ("5x0e+4x0e+3x1o", "4x0e+2x1o+6x0e", 600, 3),
+    ("260x0e+100x1o", "130x0e+260x1o", 600, 3), ("65x0e+129x1o", "63x0e+65x1o", 515, 1),
+    ("4x1o", "4x1e", 700, 2), ("8x0e", "8x0e+4x2e", 5000, 3), ("64x0e+32x3o", "64x0e+100x3o", 5000, 40)]
 
 
 def linear_inputs(irr, n, n_types, seed, padded=0.15):
