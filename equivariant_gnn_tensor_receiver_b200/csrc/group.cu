@@ -3,8 +3,8 @@
 //   perm    = node ids by key, ascending inside a key (key = type, or n_types for
 //             any other value), offsets[t] = number of nodes with a key below t.
 //
-// The N ids are cut into tiles of consecutive nodes, worked on 4096 at a time.  A
-// tile's warps own consecutive pieces of 128; the lanes of a warp that hold the same key
+// The N ids are cut into tiles of consecutive nodes, worked on up to 8192 at a time.  A
+// tile's warps own consecutive pieces of up to 256; the lanes of a warp that hold the same key
 // find each other (match) and their ranks follow from the lane order, so a node's place is
 //   offsets[key] + nodes of that key in earlier tiles + in earlier warps + rank:
 // no atomics decide an order, and the result is the stable one.
@@ -25,31 +25,33 @@ namespace {
 
 constexpr int kWarps = 32;                 // of a CTA
 constexpr int kKeys = TPCONV_MAX_TYPES + 1;
-constexpr int kSteps = 4;                  // nodes of a lane at a time
-constexpr int kSub = 32 * kWarps * kSteps; // nodes of a CTA at a time
-constexpr int kSingle = 2 * kSub;          // nodes handled by one CTA alone
-constexpr int kMaxTiles = 592;
+constexpr int kSteps = 8;                  // nodes of a lane at a time, at most
+constexpr int kStep = 32 * kWarps;         // nodes of a CTA in a step
+constexpr int kSingle = kStep * kSteps;    // nodes handled by one CTA alone
+constexpr int kMaxTiles = 296;             // two CTAs of 1024 threads per SM: one wave
 
-// the keys of the lane's nodes first, first + 32, ...; -1 behind n
-__device__ __forceinline__ void load_keys(const int* type, int64_t first, int64_t n, int T, int (&key)[kSteps]) {
+// the keys of the lane's nodes first, first + 32, ... of `steps` steps; -1 behind n
+__device__ __forceinline__ void load_keys(const int* type, int64_t first, int64_t n, int steps, int T,
+                                          int (&key)[kSteps]) {
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int64_t p = first + 32 * i;
-    const int t = p < n ? type[p] : 0;
-    key[i] = p < n ? ((t >= 0 && t < T) ? t : T) : -1;
+    const bool in = i < steps && p < n;
+    const int t = in ? type[p] : 0;
+    key[i] = in ? ((t >= 0 && t < T) ? t : T) : -1;
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) k_group_count(int64_t N, int64_t tile, int T, int tiles,
+__global__ void __launch_bounds__(kWarps * 32) k_group_count(int64_t N, int64_t tile, int steps, int T, int tiles,
                                                              const int* __restrict__ type, int* __restrict__ hist) {
   __shared__ int cnt[4][kKeys];  // (copies: less contention on a common type)
   const int K = T + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 4 * kKeys; i += blockDim.x) cnt[i / kKeys][i % kKeys] = 0;
   __syncthreads();
   const int64_t t0 = blockIdx.x * tile, t1 = min(t0 + tile, N);
-  for (int64_t s = t0; s < t1; s += kSub) {
+  for (int64_t s = t0; s < t1; s += kStep * steps) {
     int key[kSteps];
-    load_keys(type, s + warp * (32 * kSteps) + lane, t1, T, key);
+    load_keys(type, s + warp * 32 * steps + lane, t1, steps, T, key);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
       if (key[i] >= 0) atomicAdd(&cnt[warp & 3][key[i]], 1);
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_count(int64_t N, int64_t 
 
 // place of every node of one tile.  tiles == 1: the tile is everything and no
 // histogram table is read.
-__global__ void __launch_bounds__(kWarps * 32) k_group_place(int64_t N, int64_t tile, int T, int tiles,
+__global__ void __launch_bounds__(kWarps * 32, 2) k_group_place(int64_t N, int64_t tile, int steps, int T, int tiles,
                                                              const int* __restrict__ type,
                                                              const int* __restrict__ hist, int* __restrict__ perm,
                                                              int* __restrict__ offsets) {
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_place(int64_t N, int64_t 
     // key by key, the warps' lanes add up the tiles' histograms
     for (int k = warp; k < K; k += kWarps) {
       int b = 0, s = 0;
-#pragma unroll 4
+#pragma unroll 8
       for (int t = lane; t < tiles; t += 32) {
         const int h = hist[int64_t(k) * tiles + t];
         s += h;
@@ -87,9 +89,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_place(int64_t N, int64_t 
   } else {
     for (int k = threadIdx.x; k < K; k += blockDim.x) place[k] = total[k] = 0;
     __syncthreads();
-    for (int64_t s = t0; s < t1; s += kSub) {
+    for (int64_t s = t0; s < t1; s += kStep * steps) {
       int key[kSteps];
-      load_keys(type, s + warp * (32 * kSteps) + lane, t1, T, key);
+      load_keys(type, s + warp * 32 * steps + lane, t1, steps, T, key);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
         if (key[i] >= 0) atomicAdd(&total[key[i]], 1);
@@ -116,15 +118,16 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_place(int64_t N, int64_t 
     }
   }
   int* mine = cnt + warp * K;
-  for (int64_t s = t0; s < t1; s += kSub) {
-    const int64_t first = s + warp * (32 * kSteps) + lane;
+  for (int64_t s = t0; s < t1; s += kStep * steps) {
+    const int64_t first = s + warp * 32 * steps + lane;
     int key[kSteps], rank[kSteps];
-    load_keys(type, first, t1, T, key);
+    load_keys(type, first, t1, steps, T, key);
     for (int k = lane; k < K; k += 32) mine[k] = 0;
     __syncwarp();
     // ranks inside the warp's piece
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
+      if (i >= steps) break;
       const unsigned peers = __match_any_sync(0xffffffffu, key[i]);
       const int before = __popc(peers & ((1u << lane) - 1));
       rank[i] = key[i] >= 0 ? mine[key[i]] + before : 0;
@@ -151,8 +154,14 @@ __global__ void __launch_bounds__(kWarps * 32) k_group_place(int64_t N, int64_t 
   }
 }
 
-// nodes of a tile for N nodes: a multiple of kSub
-int64_t tile_nodes(int64_t N) { return ((N + kMaxTiles - 1) / kMaxTiles + kSub - 1) / kSub * kSub; }
+// steps of a CTA at a time, and nodes of a tile (a multiple of those steps)
+int steps_of(int64_t N) {
+  return int(std::min<int64_t>(kSteps, (N + int64_t(kMaxTiles) * kStep - 1) / (int64_t(kMaxTiles) * kStep)));
+}
+int64_t tile_nodes(int64_t N) {
+  const int64_t sub = int64_t(kStep) * steps_of(N);
+  return ((N + kMaxTiles - 1) / kMaxTiles + sub - 1) / sub * sub;
+}
 
 size_t place_smem(int T) { return size_t(kWarps + 2) * (T + 1) * 4; }
 static_assert((kWarps + 2) * kKeys * 4 <= 48 * 1024, "the counters fit the default shared memory");
@@ -192,15 +201,16 @@ int tpconv_group_nodes(int64_t N, int n_types, const int32_t* type, int32_t* per
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   NodePhase ph(TPCONV_PHASE_GROUP, st);
   if (N <= kSingle) {
-    k_group_place<<<1, kWarps * 32, place_smem(n_types), st>>>(N, kSingle, n_types, 1, type, nullptr, perm, offsets);
+    k_group_place<<<1, kWarps * 32, place_smem(n_types), st>>>(
+        N, kSingle, int(std::max<int64_t>(1, (N + kStep - 1) / kStep)), n_types, 1, type, nullptr, perm, offsets);
     ph.note(1);
   } else {
     const int64_t tile = tile_nodes(N);
     const int tiles = int((N + tile - 1) / tile);
     int* hist = static_cast<int*>(workspace);
-    k_group_count<<<tiles, kWarps * 32, 0, st>>>(N, tile, n_types, tiles, type, hist);
+    k_group_count<<<tiles, kWarps * 32, 0, st>>>(N, tile, steps_of(N), n_types, tiles, type, hist);
     if (cudaGetLastError()) return TPCONV_ERR_CUDA;
-    k_group_place<<<tiles, kWarps * 32, place_smem(n_types), st>>>(N, tile, n_types, tiles, type, hist, perm, offsets);
+    k_group_place<<<tiles, kWarps * 32, place_smem(n_types), st>>>(N, tile, steps_of(N), n_types, tiles, type, hist, perm, offsets);
     ph.note(2);
   }
   return cudaGetLastError() == cudaSuccess ? TPCONV_OK : TPCONV_ERR_CUDA;
