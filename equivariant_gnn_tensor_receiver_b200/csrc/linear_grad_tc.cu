@@ -90,6 +90,8 @@ struct Shared {
   int issued[kCopyWarps];
 };
 
+constexpr int kDynMax = kSMemMax - int(sizeof(Shared)) - 64;  // dynamic shared memory of a call, at most
+
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, uint64_t limit, volatile int* abort, int code) {
   return wait_or_abort(b, parity, limit, abort, &g_linear_grad_error, code);
 }
@@ -596,13 +598,14 @@ cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t l
   const int fixed = 1024 + 2 * kBTile + P.n_entries * int(sizeof(Entry) + sizeof(Cut)) + (P.T + 2) * 4;
   // at most 32 KB of x and 16 KB of g: two stages always fit; an even number, so that a stage
   // belongs to one set of converters
-  const int stages = std::min(kMaxStages, (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / stage) & ~1;
+  const int stages = std::min(kMaxStages, (kDynMax - fixed) / stage) & ~1;
   if (stages < 2) return cudaErrorInvalidValue;
   const int sm = fixed + stages * stage;
   const bool v = vec4(G);
   auto* k = split ? (v ? k_linear_grad_tc<true, 4> : k_linear_grad_tc<true, 1>)
                   : (v ? k_linear_grad_tc<false, 4> : k_linear_grad_tc<false, 1>);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+  // (the most a call may ask for, not this call's: another thread's call must not lower it)
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynMax);
   if (e) return e;
   const int ctas = ctas_of(G.p, G.n_paths, G.T, G.N);
   k<<<ctas, kThreads, sm, st>>>(P, stages, stage, sx, part, limit);

@@ -113,6 +113,8 @@ struct Shared {
   int issued[2][kCopyWarps];
 };
 
+constexpr int kDynMax = kSMemMax - int(sizeof(Shared)) - 64;  // dynamic shared memory of a call, at most
+
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, uint64_t limit, volatile int* abort, int code) {
   return wait_or_abort(b, parity, limit, abort, &g_linear_error, code);
 }
@@ -722,12 +724,13 @@ cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStr
     const int fixed = 1024 + most * kWHalf + 2 * kRaw + P.n_src * int(sizeof(LinSource)) +
                       P.n_entries * int(sizeof(Entry) + sizeof(Cut)) + (P.T + 2) * 4;
     static_assert(1024 + kMaxHalves * kWHalf + 4 * kRaw + kLinSources * int(sizeof(LinSource)) +
-                          kLinTcEntries * int(sizeof(Entry) + sizeof(Cut)) + (TPCONV_MAX_TYPES + 2) * 4 + int(sizeof(Shared)) + 64 <=
-                      kSMemMax,
+                          kLinTcEntries * int(sizeof(Entry) + sizeof(Cut)) + (TPCONV_MAX_TYPES + 2) * 4 <=
+                      kDynMax,
                   "a raw chunk always fits");
-    const int stages = std::min(kMaxStages, (kSMemMax - int(sizeof(Shared)) - 64 - fixed) / (2 * kRaw));
+    const int stages = std::min(kMaxStages, (kDynMax - fixed) / (2 * kRaw));
     const int bytes = fixed + 2 * stages * kRaw;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // (the most a call may ask for, not this call's: another thread's call must not lower it)
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynMax);
     if (e) return e;
     kernel<<<unsigned(std::min<int64_t>(kSMs, tiles)), kThreads, bytes, st>>>(P, most, stages, limit);
     if ((e = cudaGetLastError())) return e;

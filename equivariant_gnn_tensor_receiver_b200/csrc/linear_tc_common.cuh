@@ -14,14 +14,7 @@ __device__ __forceinline__ void mma_tf32_ta(uint32_t d, uint32_t a, uint64_t b, 
       " tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-// 8 / 16 fp32 per lane into consecutive TMEM columns of the warp's lanes
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-               : "memory");
-}
+// 16 fp32 per lane into consecutive TMEM columns of the warp's lanes
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -66,11 +59,11 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Brings the node ids some tiles ahead into L2: a tile is copied in less time than HBM
-// answers, so that reading them one tile ahead alone would bound the copies.
+// Brings the node ids some tiles ahead into L2: a tile's copies are issued in less time than
+// HBM answers, so that reading the ids one tile ahead alone would bound them.
 constexpr int kPermAhead = 512;
 __device__ __forceinline__ void prefetch_nodes(const int* perm, int at, int64_t N) {
-  if (at < N) asm volatile("prefetch.global.L2 [%0];" ::"l"(perm + at));
+  if (at >= 0 && at < N) asm volatile("prefetch.global.L2 [%0];" ::"l"(perm + at));
 }
 
 // untiled bulk copies: both addresses and the size are multiples of 16 bytes

@@ -474,7 +474,9 @@ cudaError_t launch(const NormDev& p, const NormArgs& a, int grid, cudaStream_t s
   const int sums = MODE == kFwd ? 0 : kThreads(TL) / TL / 2 * (MODE == kBwd ? 2 : 1);
   const size_t sm = std::max(size_t(MODE == kDbl ? 3 : 2) * dimp + red_floats<TL>(), size_t(sums) * dimp) * 4;
   if (sm > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(k_norm<MODE, VEC, V, TL>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sm));
+    // (the most a call may ask for, not this call's: another thread's call must not lower it)
+    cudaError_t e = cudaFuncSetAttribute(k_norm<MODE, VEC, V, TL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         227 * 1024);
     if (e) return e;
   }
   k_norm<MODE, VEC, V, TL><<<grid, kThreads(TL), sm, st>>>(p, a);

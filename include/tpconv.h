@@ -255,8 +255,7 @@ int tpconv_double_backward(const tpconv_plan* plan, int64_t N, int64_t E, const 
  * linear map and the layer norm of irreps features.  Features and conventions
  * are those at the top of this file (fp32, contiguous, [mul][2l+1] blocks,
  * caller-owned memory, asynchronous on the stream, outputs overwritten).
- * They need no one-time device set-up, so their first call may be a captured
- * one.  No output may overlap an input or another output
+ * They need no one-time device set-up: their first call may be a captured one.  No output may overlap an input or another output
  * (TPCONV_ERR_INVALID_ARG).  The pages define none of them: they are additions
  * of this library (what a layer of such a network holds next to the
  * convolution), with formulas of their own below.
@@ -284,10 +283,16 @@ int tpconv_group_nodes(int64_t N, int n_types, const int32_t* type, int32_t* per
  * perm / offsets come from tpconv_group_nodes for the same N and n_types.
  * (Entries outside [0, N] are never followed; the rows they stand for are
  * then undefined.)
- *   gemm: TPCONV_GEMM_FP32 / _TF32 / _SIMT as in tpconv_options.  The tensor-
- *   core modes need blocks whose multiplicities are multiples of 4, rows a
- *   multiple of 16 bytes and 16-byte aligned tensors; other calls run on the
- *   FP32 pipes, whatever the mode. */
+ *   gemm: TPCONV_GEMM_FP32 / _TF32 / _SIMT as in tpconv_options, for any
+ *   multiplicities and alignment (blocks whose multiplicities are multiples of
+ *   4 in 16-byte aligned tensors run fastest).  Small calls, and plans with more
+ *   than 48 (output block, 64 channels) or (path, 128 x 64 channels) pairs, run
+ *   on the FP32 pipes whatever the mode.  In the tensor-core modes an infinity,
+ *   or a value that rounds to one in TF32 (above 3.4e38), may come out as NaN
+ *   where it enters: its node's row, its type's dweight, a weight's channel.
+ *   Multiplicities are at most 8192, paths at most 48.  Kernel waits are bounded
+ *   as described at tpconv_get_device_status; tpconv_linear_device_status
+ *   reports them. */
 typedef struct tpconv_linear tpconv_linear;
 int tpconv_linear_create(tpconv_linear** out, const char* irreps_in, const char* irreps_out,
                          int n_types, int gemm);

@@ -479,3 +479,74 @@ def test_expired_waits_are_reported_and_recovered(T):
     got = (T.linear_forward(p, G, x, w), T.linear_backward(p, G, x, w, g, want=("dweight",))["dweight"])
     assert L.tpconv_linear_device_status(p) == L.TPCONV_OK
     assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+import equivariant_gnn_tensor_receiver_b200 as T
+irr, n = "48x0e+16x1o", 1500
+x = torch.randn(n, 96, device="cuda")
+types = torch.randint(-1, 3, (n,), device="cuda", dtype=torch.int32)
+norm, lin = T.EquivariantNorm(irr), T.TypedLinear(irr, irr, 3)
+x.requires_grad_(True)
+params = [x, norm.weight, norm.bias, lin.weight]
+
+def step():
+    groups = T.NodeGroups(types, 3)
+    out = lin(norm(x), groups)
+    first = torch.autograd.grad(out.square().sum(), params, create_graph=True)
+    second = torch.autograd.grad(first[0].square().sum(), params)
+    return [out, *first, *second]
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):   # the first call of every kernel
+    held = step()
+for _ in range(2):
+    with torch.no_grad():
+        x.copy_(torch.randn_like(x))
+        types.copy_(torch.randint(-1, 3, (n,), device="cuda", dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(held, step()):
+        assert torch.equal(a, b)
+print("captured ok")
+"""
+
+
+def test_first_calls_may_be_captured():
+    """A fresh process whose first call of every operator is a captured one, first and second order; the replays
+    on new features and new types agree bit for bit with eager calls."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stdout + r.stderr
+
+
+def test_two_streams_at_once(T):
+    """the same plan, groups and weights from two streams at a time, each call with a workspace of its own"""
+    import torch
+    irr = ("64x0e+64x1o",) * 2
+    t, d = linear_inputs(irr, 3000, 5, 4)
+    p, q = T.LinearPlan(*irr, n_types=5), T.NormPlan(irr[0])
+    G = T.NodeGroups(dev(t, torch.int32), 5)
+    x, w, g, a = dev(d["x"]), dev(d["w"]), dev(d["g"]), dev(d["a"])
+
+    def run(v, stream=None):
+        r = T.linear_backward(p, G, v, w, g, stream=stream)
+        s = T.norm_backward(q, v, None, g, stream=stream)
+        return [r["dx"], r["dweight"], s["dx"], s["dweight"], s["dbias"]]
+
+    want = [[u.clone() for u in run(v)] for v in (x, a)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, v in enumerate((x, a)):
+            got[i].append(run(v, streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(u, v) for u, v in zip(r, want[i]))
