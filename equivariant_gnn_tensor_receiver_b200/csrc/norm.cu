@@ -24,6 +24,11 @@
 // atomics: repeated calls agree bit for bit).  (Lanes dealt out over the row without
 // regard to blocks need a masked sum per block and quantity: 46 us against 25
 // for the double backward of 20 011 rows of 37x0e+21x1o+5x2e+3x0o.)
+//
+// Measured (graph replays, warm; floor = bytes over 6.54 TB/s), 120 000 rows: 128x l<=3
+// (2048 floats) forward 312 us (floor 301), backward 548 (451), double backward 843 (752);
+// 32x l<=2 (288 floats) 53 (42), 92 (63), 144 (106).  Odd rows (143 floats, read 4 bytes at
+// a time) 42 (19), 66 (28), 117 (47): there the loads in flight bound it, not HBM.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -203,17 +208,39 @@ __global__ void __launch_bounds__(kThreads(TL)) k_norm(const __grid_constant__ N
   // every lane runs the same number of rounds: the sums are collective
   const int64_t stride = int64_t(gridDim.x) * TEAMS;
   const int64_t rounds = (A.n + stride - 1) / stride;
+  constexpr int NG = MODE == kFwd ? 1 : V, NA = MODE == kDbl ? V : 1;
+  auto load = [&](int64_t k, Pack<VEC>(&x)[V], Pack<VEC>(&g)[NG], Pack<VEC>(&a)[NA]) {
+    const int64_t row = k * stride + int64_t(blockIdx.x) * TEAMS + team, base = row * p.dim + col;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const bool in = row < A.n && j * step < left;
+      x[j] = in ? ld_row<VEC>(A.x + base + j * step) : zero;
+      if constexpr (MODE != kFwd) g[j] = in ? ld_row<VEC>(A.g + base + j * step) : zero;
+      if constexpr (MODE == kDbl) a[j] = (in && A.a) ? ld_row<VEC>(A.a + base + j * step) : zero;
+    }
+  };
+  // Rows of few floats a lane are read one round ahead: a warp's own latencies (the reads,
+  // then the sums one after another) would leave HBM waiting.  120 000 rows of 128x l<=3,
+  // without and with: backward 887 and 548 us, double backward 1244 and 843; 32x l<=2: 122
+  // and 92, 170 and 144.  Not for single floats in the double backward: 122 without, 136 with.
+  constexpr bool AHEAD = V * VEC <= 12 && (VEC == 4 || MODE != kDbl);
+  Pack<VEC> nx[V], ng[NG], na[NA];
+  if constexpr (AHEAD) load(0, nx, ng, na);
   for (int64_t k = 0; k < rounds; ++k) {
     const int64_t row = k * stride + int64_t(blockIdx.x) * TEAMS + team;
     const bool on = row < A.n;
     const int64_t base = row * p.dim + col;
-    Pack<VEC> x[V], g[MODE == kFwd ? 1 : V], a[MODE == kDbl ? V : 1];
+    Pack<VEC> x[V], g[NG], a[NA];
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const bool in = on && j * step < left;
-      x[j] = in ? ld_row<VEC>(A.x + base + j * step) : zero;
-      if constexpr (MODE != kFwd) g[j] = in ? ld_row<VEC>(A.g + base + j * step) : zero;
-      if constexpr (MODE == kDbl) a[j] = (in && A.a) ? ld_row<VEC>(A.a + base + j * step) : zero;
+      for (int j = 0; j < V; ++j) {
+        x[j] = nx[j];
+        if constexpr (MODE != kFwd) g[j] = ng[j];
+        if constexpr (MODE == kDbl) a[j] = na[j];
+      }
+      load(k + 1, nx, ng, na);
+    } else {
+      load(k, x, g, a);
     }
     // centre the scalars (x, and gg_x in the double backward); what lies behind a block stays 0
     if (p.any0) {
@@ -451,11 +478,13 @@ Shape shape_of(NormDev& p, bool vec4) {
 int teams_of(int tl) { return kThreads(tl) / tl; }
 
 // CTAs of a pass.  Forward: as many as there are rows for, up to eight per SM.  The
-// gradients: two per SM (what their registers leave resident), and at least two rows to
-// a team: the partial rows of the sums are paid once for them.
-int grid_of(int64_t n, int tl, int mode) {
-  const int64_t teams = mode == kFwd ? n : (n + 1) / 2, ctas = (teams + teams_of(tl) - 1) / teams_of(tl);
-  return int(std::max<int64_t>(1, std::min<int64_t>(ctas, int64_t(kSMs) * (mode == kFwd ? 8 : 2))));
+// gradients: what their registers leave resident (512 threads per SM, 1024 of few
+// floats a lane), and at least two rows to a team: the partial rows of the sums are
+// paid once for them.
+int grid_of(int64_t n, const Shape& s, int mode) {
+  const int64_t teams = mode == kFwd ? n : (n + 1) / 2, ctas = (teams + teams_of(s.tl) - 1) / teams_of(s.tl);
+  const int per_sm = mode == kFwd ? 8 : (s.vec * s.v <= 12 ? 1024 : 512) / kThreads(s.tl);
+  return int(std::max<int64_t>(1, std::min<int64_t>(ctas, int64_t(kSMs) * per_sm)));
 }
 
 int reduce_grid(const NormDev& p) {
@@ -538,7 +567,7 @@ size_t partial_bytes(const tpconv_norm* plan, int op, int64_t N) {
   NormDev p = plan->p;
   const Shape s = shape_of(p, plan->vec4), s1 = shape_of(p, false);
   const int mode = op == TPCONV_OP_BACKWARD ? kBwd : kDbl;
-  return size_t(std::max(grid_of(N, s.tl, mode), grid_of(N, s1.tl, mode))) * (mode == kBwd ? 2 : 1) * ((plan->p.dim + 3) & ~3) * 4;
+  return size_t(std::max(grid_of(N, s, mode), grid_of(N, s1, mode))) * (mode == kBwd ? 2 : 1) * ((plan->p.dim + 3) & ~3) * 4;
 }
 
 bool rows16(const tpconv_norm* plan, std::initializer_list<const void*> ps) {
@@ -637,7 +666,7 @@ int tpconv_norm_forward(const tpconv_norm* plan, int64_t N, const float* x, cons
   NormArgs a{};
   a.x = x, a.w = weight, a.b = bias, a.o0 = y, a.n = N;
   ph.note(1);
-  return status_of(launch_mode<kFwd>(s, p, a, grid_of(N, s.tl, kFwd), st));
+  return status_of(launch_mode<kFwd>(s, p, a, grid_of(N, s, kFwd), st));
 }
 
 int tpconv_norm_backward(const tpconv_norm* plan, int64_t N, const float* x, const float* weight, const float* g,
@@ -663,7 +692,7 @@ int tpconv_norm_backward(const tpconv_norm* plan, int64_t N, const float* x, con
   if (!dx && !sums) return TPCONV_OK;
   NodePhase ph(TPCONV_PHASE_NORM, st);
   const Shape s = shape_of(p, rows16(plan, {x, g, dx}));
-  const int grid = grid_of(N, s.tl, kBwd);
+  const int grid = grid_of(N, s, kBwd);
   NormArgs a{};
   a.x = x, a.w = weight, a.g = g, a.o0 = dx, a.n = N;
   a.want_b = dbias && p.nbias > 0;
@@ -700,7 +729,7 @@ int tpconv_norm_double_backward(const tpconv_norm* plan, int64_t N, const float*
   if (!d_g && !d_x && !d_weight) return TPCONV_OK;
   NodePhase ph(TPCONV_PHASE_NORM, st);
   const Shape s = shape_of(p, rows16(plan, {x, g, gg_x, d_g, d_x}));
-  const int grid = grid_of(N, s.tl, kDbl);
+  const int grid = grid_of(N, s, kDbl);
   NormArgs a{};
   a.x = x, a.w = weight, a.g = g, a.a = gg_x, a.al = gg_weight, a.be = gg_bias, a.o0 = d_g, a.o1 = d_x, a.n = N;
   a.part = d_weight ? static_cast<float*>(workspace) : nullptr;
