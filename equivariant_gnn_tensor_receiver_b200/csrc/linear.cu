@@ -18,6 +18,7 @@
 #include <new>
 #include <vector>
 
+#include "chain.cuh"
 #include "irreps.h"
 #include "linear_grad_tc.h"
 #include "linear_tc.h"
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(256) k_linear_grad(const __grid_constant__ Lin
                                                      int tiles_w, float* __restrict__ part) {
   __shared__ float sa[kTK][kTR + 4], sb[kTK][kTC + 4];
   __shared__ int s_first, s_count;
+  chain_next();
   const int per = tiles_u * tiles_w;
   const LinPath& Q = P.p[blockIdx.y / per];
   const int u0 = ((blockIdx.y % per) / tiles_w) * kTR, w0 = ((blockIdx.y % per) % tiles_w) * kTC;
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(256) k_linear_grad(const __grid_constant__ Lin
 
 // dW[t][i] = sum of part[piece][i] over the pieces of type t = blockIdx.y, in order
 __global__ void __launch_bounds__(256) k_linear_grad_reduce(const __grid_constant__ LinGrad P, int unit,
-                                                            const float* __restrict__ part) {
+                                                            const float* part) {
   __shared__ int s_lo, s_n;
   const int t = blockIdx.y;
   if (threadIdx.x < 32) {
@@ -213,6 +215,7 @@ __global__ void __launch_bounds__(256) k_linear_grad_reduce(const __grid_constan
     if (threadIdx.x == 0) s_lo = before, s_n = n;
   }
   __syncthreads();
+  chain_wait();
   for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < P.wnumel; i += 256LL * gridDim.x) {
     float s = 0.f;
     for (int k = 0; k < s_n; ++k) s += part[int64_t(s_lo + k) * P.wnumel + i];
@@ -296,12 +299,22 @@ double mega_macs(const tpconv_linear* p, int64_t N) {
   return m * 1e-6 * double(N);
 }
 
+// Whether a call's products are chained (chain.cuh).  Its tensor-core kernels take a whole SM
+// for each CTA: chained, the next one's preparation hides in the tail of the one before; for
+// more rows its early CTAs cost more than that.  Backward with 8 types, apart and chained in
+// us: 64x0e+64x1o+64x2e, 4096 nodes 47 / 45, 8192 nodes 59 / 55, 16384 nodes 83 / 85, 262144
+// nodes 614 / 820; 128x up to l = 3, 4096 nodes 102 / 102, 8192 nodes 151 / 159.  (The join
+// of partial tiles, of small CTAs, is always chained.)
+bool chained(const tpconv_linear* p, int64_t N) { return N * std::max(p->dim_in, p->dim_out) <= 5000000; }
+
 // Small products run on the FP32 pipes whatever the mode (and are no less exact): the
 // tensor-core kernel takes 8 to 9 us before its first tile is stored.  Measured, FP32 /
 // tensor cores in us: 8 channels, 64 to 4096 nodes 8.3 / 12.4; 32 channels, 512 nodes
 // 10.3 / 12.4, 1024 nodes 13 / 12.4; 64 channels, 32 nodes 18.4 / 12.3 (its depth is
 // walked 16 channels a step).
-cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph, cudaStream_t st) {
+// after, more: a kernel of the same call was the last work on the stream, another one follows.
+cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph, bool after, bool more,
+                         cudaStream_t st) {
   int depth = 0;  // most channels that an output block sums over
   for (int b = 0; b < R.n_out; ++b) {
     int k = 0;
@@ -312,7 +325,7 @@ cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph
   const int tc = p->gemm != TPCONV_GEMM_SIMT && !small ? linear_tc_launches(R) : 0;
   if (tc > 0) {
     ph.note(tc);
-    return linear_tc_rows(R, p->gemm == TPCONV_GEMM_FP32, device_wait_limit(), st);
+    return linear_tc_rows(R, p->gemm == TPCONV_GEMM_FP32, device_wait_limit(), after, more, st);
   }
   int colt = 1, dmax = 1;
   for (int b = 0; b < R.n_out; ++b) {
@@ -330,7 +343,8 @@ cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph
 // 64x0e+64x1o+64x2e, 64 nodes 14.4 / 16.5, 512 nodes 18.5 / 19.1 (8 types) and 18.5 / 22.6
 // (one); 128 channels up to l = 3, 32 nodes 16.5 / 18.5, 512 nodes 43 / 27.
 cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, const int* offsets, const float* x,
-                            const float* g, float* dw, float* part, NodePhase& ph, cudaStream_t st) {
+                            const float* g, float* dw, float* part, NodePhase& ph, bool after,
+                            cudaStream_t st) {
   if (p->wnumel == 0) return cudaSuccess;
   LinGrad G;
   std::memset(&G, 0, sizeof(G));
@@ -341,7 +355,7 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
   const bool small = N <= 512 && mega_macs(p, N) <= 20;
   if (p->gemm != TPCONV_GEMM_SIMT && !small && linear_grad_tc_supported(G)) {
     ph.note(2);
-    return linear_grad_tc(G, p->gemm == TPCONV_GEMM_FP32, part, device_wait_limit(), st);
+    return linear_grad_tc(G, p->gemm == TPCONV_GEMM_FP32, part, device_wait_limit(), after, st);
   }
   int cu = 1, cw = 1;
   for (int i = 0; i < p->n_paths; ++i) {
@@ -356,9 +370,8 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
   cudaError_t e = cudaGetLastError();
   if (e) return e;
   const unsigned bx = unsigned(std::min<int64_t>((p->wnumel + 255) / 256, 1024));
-  k_linear_grad_reduce<<<dim3(bx, unsigned(p->T)), 256, 0, st>>>(G, unit, part);
   ph.note(2);
-  return cudaGetLastError();
+  return chain_launch(k_linear_grad_reduce, dim3(bx, unsigned(p->T)), 256, 0, st, G, unit, static_cast<const float*>(part));
 }
 
 size_t ws_bytes(const tpconv_linear* p, int op, int64_t N) {
@@ -510,7 +523,7 @@ int tpconv_linear_forward(const tpconv_linear* plan, int64_t N, const int32_t* p
   LinRows R;
   fill_rows(plan, false, 1, &R);
   R.N = N, R.x[0] = x, R.w[0] = weight, R.out = out, R.perm = perm, R.offsets = offsets;
-  return status_of(rows_product(plan, R, ph, s));
+  return status_of(rows_product(plan, R, ph, false, false, s));
 }
 
 int tpconv_linear_backward(const tpconv_linear* plan, int64_t N, const int32_t* perm, const int32_t* offsets,
@@ -529,14 +542,16 @@ int tpconv_linear_backward(const tpconv_linear* plan, int64_t N, const int32_t* 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (N == 0) return (dweight && wb && cudaMemsetAsync(dweight, 0, wb, s)) ? TPCONV_ERR_CUDA : TPCONV_OK;
   NodePhase ph(TPCONV_PHASE_LINEAR, s);
+  const bool chain = chained(plan, N);
   cudaError_t e = cudaSuccess;
   if (dx) {
     LinRows R;
     fill_rows(plan, true, 1, &R);
     R.N = N, R.x[0] = g, R.w[0] = weight, R.out = dx, R.perm = perm, R.offsets = offsets;
-    e = rows_product(plan, R, ph, s);
+    e = rows_product(plan, R, ph, false, chain && dweight && plan->wnumel, s);
   }
-  if (!e && dweight) e = weight_gradient(plan, N, perm, offsets, x, g, dweight, static_cast<float*>(workspace), ph, s);
+  if (!e && dweight)
+    e = weight_gradient(plan, N, perm, offsets, x, g, dweight, static_cast<float*>(workspace), ph, chain && dx, s);
   return status_of(e);
 }
 
@@ -563,6 +578,9 @@ int tpconv_linear_double_backward(const tpconv_linear* plan, int64_t N, const in
   NodePhase ph(TPCONV_PHASE_LINEAR, s);
   cudaError_t e = cudaSuccess;
   LinRows R;
+  // products of this call, each but the last followed by another on the stream
+  const bool chain = chained(plan, N);
+  const bool p_g = d_g && (a || b), p_x = d_x && b, p_w = d_weight && a && plan->wnumel;
   if (d_g) {
     if (!a && !b) {
       e = cudaMemsetAsync(d_g, 0, rout, s);
@@ -571,7 +589,7 @@ int tpconv_linear_double_backward(const tpconv_linear* plan, int64_t N, const in
       R.N = N, R.out = d_g, R.perm = perm, R.offsets = offsets;
       R.x[0] = a ? gg_x : x, R.w[0] = a ? weight : gg_weight;
       R.x[1] = x, R.w[1] = gg_weight;
-      e = rows_product(plan, R, ph, s);
+      e = rows_product(plan, R, ph, false, chain && (p_x || (p_w && !d_x)), s);
     }
   }
   if (!e && d_x) {
@@ -580,11 +598,12 @@ int tpconv_linear_double_backward(const tpconv_linear* plan, int64_t N, const in
     } else {
       fill_rows(plan, true, 1, &R);
       R.N = N, R.x[0] = g, R.w[0] = gg_weight, R.out = d_x, R.perm = perm, R.offsets = offsets;
-      e = rows_product(plan, R, ph, s);
+      e = rows_product(plan, R, ph, chain && p_g, chain && p_w, s);
     }
   }
   if (!e && d_weight && a)
-    e = weight_gradient(plan, N, perm, offsets, gg_x, g, d_weight, static_cast<float*>(workspace), ph, s);
+    e = weight_gradient(plan, N, perm, offsets, gg_x, g, d_weight, static_cast<float*>(workspace), ph,
+                        chain && (p_x || (p_g && !d_x)), s);
   return status_of(e);
 }
 

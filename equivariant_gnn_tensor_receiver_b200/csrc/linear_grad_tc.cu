@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "chain.cuh"
 #include "linear_grad_tc.h"
 #include "linear_tc_common.cuh"
 
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  chain_next();
   for (int i = threadIdx.x; i < P.n_entries * int(sizeof(Entry) / 4); i += kThreads)
     reinterpret_cast<int*>(E)[i] = reinterpret_cast<const int*>(P.e)[i];
   for (int i = threadIdx.x; i < P.n_entries * int(sizeof(Cut) / 4); i += kThreads)
@@ -461,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 30) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
+    chain_wait();
   }
 }
 
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinRows = 16;  // 16 float4 of 64 columns a row: 256 threads
 static_assert(kJoinRows * kNT / 4 == 256, "one float4 a thread");
 __global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant__ Params P, int ctas,
-                                                          const float* __restrict__ part) {
+                                                          const float* part) {
   __shared__ int offs[TPCONV_MAX_TYPES + 2];
   __shared__ int total[4], s_slots, slot[kSMs];
   const int t = blockIdx.x % P.T, e = blockIdx.x / P.T, warp = threadIdx.x >> 5;
@@ -482,6 +485,7 @@ __global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant_
     if ((threadIdx.x & 31) == 0) total[warp] = n;
   }
   __syncthreads();
+  chain_wait();
   const int r0 = blockIdx.y * kJoinRows, r1 = min(L.cu, r0 + kJoinRows), cw = L.cw;
   if (r0 >= r1) return;
   if (warp == 0) {
@@ -568,7 +572,7 @@ size_t linear_grad_tc_bytes(const LinPath* path, int n, int T, int64_t N) {
   return size_t(2) * ctas_of(path, n, T, N) * kMT * kNT * 4;
 }
 
-cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t limit, cudaStream_t st) {
+cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t limit, bool after, cudaStream_t st) {
   Params P;
   std::memset(&P, 0, sizeof(P));
   P.T = G.T, P.dim_x = G.dim_x, P.dim_g = G.dim_g, P.N = G.N, P.wnumel = G.wnumel;
@@ -611,10 +615,14 @@ cudaError_t linear_grad_tc(const LinGrad& G, bool split, float* part, uint64_t l
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynMax);
   if (e) return e;
   const int ctas = ctas_of(G.p, G.n_paths, G.T, G.N);
-  k<<<ctas, kThreads, sm, st>>>(P, stages, stage, sx, part, limit);
-  if ((e = cudaGetLastError())) return e;
-  k_linear_grad_join<<<dim3(unsigned(P.n_entries * G.T), kMT / kJoinRows), 256, 0, st>>>(P, ctas, part);
-  return cudaGetLastError();
+  if (after) {
+    if ((e = chain_launch(k, ctas, kThreads, sm, st, P, stages, stage, sx, part, limit))) return e;
+  } else {
+    k<<<ctas, kThreads, sm, st>>>(P, stages, stage, sx, part, limit);
+    if ((e = cudaGetLastError())) return e;
+  }
+  return chain_launch(k_linear_grad_join, dim3(unsigned(P.n_entries * G.T), kMT / kJoinRows), 256, 0, st, P, ctas,
+                      static_cast<const float*>(part));
 }
 
 cudaError_t linear_grad_tc_read_error(int* code) {

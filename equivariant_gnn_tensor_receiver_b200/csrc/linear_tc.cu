@@ -37,7 +37,7 @@
 // pipe to take them: 306 us against 270 at 262144 nodes of 64x0e+64x1o+64x2e, where equal
 // shares took 270; both warpgroups of a role on one tile: 340 us.)
 // Measured (device, 3xTF32): 262144 nodes of 64x0e+64x1o+64x2e, 10 types: 239 us, 5.05 TB/s,
-// 0.77 of the measured copy rate; 4096 nodes of it: 17 us, most of it the latency of a
+// 0.77 of the measured copy rate; 4096 nodes of it: 21 us, most of it the latency of a
 // CTA's first tile (weight, rows, product, store one after another).
 // A sum over more than 160 channels runs in several passes that add to the output.
 // Every wait is bounded by the call's limit; on expiry the kernel records it, stops
@@ -49,6 +49,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "chain.cuh"
 #include "linear_tc.h"
 #include "linear_tc_common.cuh"
 
@@ -226,7 +227,7 @@ struct __align__(16) Four {
 
 template <bool SPLIT, int VEC>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_linear_tc(const __grid_constant__ Params P, int halves, int stages, uint64_t limit) {
+    k_linear_tc(const __grid_constant__ Params P, int halves, int stages, int more, uint64_t limit) {
   using Pack = std::conditional_t<VEC == 4, Four, One>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base =
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (more) chain_next();
   // the lists to shared memory: a walk through kernel parameters misses the constant cache at every step
   for (int i = threadIdx.x; i < P.n_src * int(sizeof(LinSource) / 4); i += kThreads)
     reinterpret_cast<int*>(S)[i] = reinterpret_cast<const int*>(P.s)[i];
@@ -630,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 21) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
+    chain_wait();
   }
 }
 
@@ -672,7 +675,7 @@ int linear_tc_launches(const LinRows& R) {
   return entries <= kLinTcEntries ? passes : 0;
 }
 
-cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStream_t st) {
+cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, bool after, bool more, cudaStream_t st) {
   const bool v = vec4(R);
   auto* kernel = split ? (v ? k_linear_tc<true, 4> : k_linear_tc<true, 1>)
                        : (v ? k_linear_tc<false, 4> : k_linear_tc<false, 1>);
@@ -735,8 +738,15 @@ cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, cudaStr
     // (the most a call may ask for, not this call's: another thread's call must not lower it)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynMax);
     if (e) return e;
-    kernel<<<unsigned(std::min<int64_t>(kSMs, tiles)), kThreads, bytes, st>>>(P, most, stages, limit);
-    if ((e = cudaGetLastError())) return e;
+    const unsigned grid = unsigned(std::min<int64_t>(kSMs, tiles));
+    const int next = more && pass == passes - 1;
+    if (after && pass == 0) {  // (a later pass reads what the one before wrote)
+      e = chain_launch(kernel, grid, kThreads, bytes, st, P, most, stages, next, limit);
+    } else {
+      kernel<<<grid, kThreads, bytes, st>>>(P, most, stages, next, limit);
+      e = cudaGetLastError();
+    }
+    if (e) return e;
   }
   return cudaSuccess;
 }

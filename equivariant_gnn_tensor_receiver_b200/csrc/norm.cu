@@ -38,6 +38,7 @@
 #include <vector>
 
 #include "../../include/tpconv.h"
+#include "chain.cuh"
 #include "irreps.h"
 #include "node_ops.h"
 
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kThreads(TL)) k_norm(const __grid_constant__ N
   constexpr int NACC = MODE == kBwd ? 2 : (MODE == kDbl ? 1 : 0);  // dw, db | d_w
   extern __shared__ float4 smem4[];
   float* sm = reinterpret_cast<float*>(smem4);
+  if (MODE != kFwd && A.part) chain_next();
   const int dimp = (p.dim + 3) & ~3;
   float* sw = sm;                                    // weight of every column
   float* s1 = sm + dimp;                             // forward: bias; double backward: gg_w
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kThreads(TL)) k_norm(const __grid_constant__ N
 // rows.  A CTA takes whole channels of one block, up to 32 columns: thread (x, y) adds
 // rows y, y + 32, ... of column x (coalesced), the 32 sums of a column are added by a
 // tree, then the 2l+1 columns of a channel: a fixed order.
-__global__ void __launch_bounds__(1024) k_norm_reduce(const __grid_constant__ NormDev p, const float* __restrict__ part,
+__global__ void __launch_bounds__(1024) k_norm_reduce(const __grid_constant__ NormDev p, const float* part,
                                                       int rows, int na, float* __restrict__ dw, float* __restrict__ db) {
   __shared__ float s[32][33], col[32];
   const int dimp = (p.dim + 3) & ~3, x = threadIdx.x & 31, y = threadIdx.x >> 5;
@@ -424,6 +426,7 @@ __global__ void __launch_bounds__(1024) k_norm_reduce(const __grid_constant__ No
   }
   const int d = p.d[b], per = 32 / d, mul = (p.off[b + 1] - p.off[b]) / d;
   const int u0 = i * per, n = min(per, mul - u0), c0 = p.off[b] + u0 * d;
+  chain_wait();
   for (int k = 0; k < na; ++k) {
     float* o = k == 0 ? (dw ? dw + p.woff[b] : nullptr) : ((db && p.boff[b] >= 0) ? db + p.boff[b] : nullptr);
     if (!o) continue;
@@ -700,9 +703,9 @@ int tpconv_norm_backward(const tpconv_norm* plan, int64_t N, const float* x, con
   cudaError_t e = launch_mode<kBwd>(s, p, a, grid, st);
   ph.note(1);
   if (e == cudaSuccess && sums) {
-    k_norm_reduce<<<reduce_grid(p), 1024, 0, st>>>(p, a.part, grid, a.want_b ? 2 : 1, dweight, dbias);
+    e = chain_launch(k_norm_reduce, reduce_grid(p), 1024, 0, st, p, static_cast<const float*>(a.part), grid,
+                     a.want_b ? 2 : 1, dweight, dbias);
     ph.note(1);
-    e = cudaGetLastError();
   }
   return status_of(e);
 }
@@ -736,9 +739,9 @@ int tpconv_norm_double_backward(const tpconv_norm* plan, int64_t N, const float*
   cudaError_t e = launch_mode<kDbl>(s, p, a, grid, st);
   ph.note(1);
   if (e == cudaSuccess && d_weight) {
-    k_norm_reduce<<<reduce_grid(p), 1024, 0, st>>>(p, a.part, grid, 1, d_weight, nullptr);
+    e = chain_launch(k_norm_reduce, reduce_grid(p), 1024, 0, st, p, static_cast<const float*>(a.part), grid, 1, d_weight,
+                     static_cast<float*>(nullptr));
     ph.note(1);
-    e = cudaGetLastError();
   }
   return status_of(e);
 }

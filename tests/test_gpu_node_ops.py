@@ -550,3 +550,60 @@ def test_two_streams_at_once(T):
     for i in range(2):
         for r in got[i]:
             assert all(torch.equal(u, v) for u, v in zip(r, want[i]))
+
+
+@pytest.mark.parametrize("n", [40, 700, 5000, 40000])
+def test_gradients_together_and_one_by_one(T, n):
+    """The kernels of one call overlap: all gradients together, call after call with one workspace and changing
+    inputs, each read at once by work behind it, equal the gradients asked for alone, bit for bit; eagerly and
+    captured."""
+    import torch
+    irr = ("64x0e+32x1o+8x2e",) * 2
+    t, d = linear_inputs(irr, n, 7, 6)
+    p, q = T.LinearPlan(*irr, n_types=7), T.NormPlan(irr[0])
+    G = T.NodeGroups(dev(t, torch.int32), 7)
+    w = dev(d["w"])
+    v = dev(f32(rng(5).normal(size=w.shape)))
+    rows = [dev(d[k]) for k in ("x", "g", "a")]
+
+    def bytes_of(plan, op):
+        return max(plan.workspace_bytes(op, n), 256)
+
+    ws = torch.empty(max(bytes_of(k, o) for k in (p, q) for o in (1, 2)), dtype=torch.uint8, device="cuda")
+
+    def together(x, g, a):
+        b = T.linear_backward(p, G, x, w, g, ws=ws)
+        c = T.linear_double_backward(p, G, x, w, g, gg_x=a, gg_weight=v, ws=ws)
+        e = T.norm_backward(q, x, None, g, ws=ws)
+        f = T.norm_double_backward(q, x, None, g, gg_x=a, ws=ws)
+        return [u.clone() for r in (b, c, e, f) for u in r.values()]
+
+    def alone(x, g, a):
+        out = []
+        for k in ("dx", "dweight"):
+            out.append(T.linear_backward(p, G, x, w, g, want=(k,))[k])
+            torch.cuda.synchronize()
+        for k in ("d_g", "d_x", "d_weight"):
+            out.append(T.linear_double_backward(p, G, x, w, g, gg_x=a, gg_weight=v, want=(k,))[k])
+            torch.cuda.synchronize()
+        for k in ("dx", "dweight", "dbias"):
+            out.append(T.norm_backward(q, x, None, g, want=(k,))[k])
+            torch.cuda.synchronize()
+        for k in ("d_g", "d_x", "d_weight"):
+            out.append(T.norm_double_backward(q, x, None, g, gg_x=a, want=(k,))[k])
+            torch.cuda.synchronize()
+        return out
+
+    turns = [(rows[i % 3], rows[(i + 1) % 3], rows[(i + 2) % 3]) for i in range(3)]
+    want = [alone(*r) for r in turns]
+    got = [together(*turns[i % 3]) for i in range(9)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [together(*r) for r in turns]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for i, r in enumerate(got + held):
+        assert len(r) == len(want[i % 3])
+        for u, z in zip(r, want[i % 3]):
+            assert torch.equal(u, z)
