@@ -13,7 +13,7 @@
 // order), then every tile adds up the histograms before its own (a table of
 // (n_types + 1) x tiles ints that stays in L2) and scatters.  Work: 4 bytes read twice
 // and 4 written per node.
-// Measured (device): 1.2 M nodes of 10 types 27 us, of which the second launch takes 22 (it
+// Measured (device): 1.2 M nodes of 89 types 27 us, of which the second launch takes 22 (it
 // waits on its matches and barriers; the bytes alone are 2 us); up to 8192 nodes 8.3 us.
 #include <cuda_runtime.h>
 
