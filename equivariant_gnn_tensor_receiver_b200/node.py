@@ -92,6 +92,8 @@ _HERE = _Here()
 def _on(dev, stream, *tensors):
     if stream is None and dev == torch.cuda.current_device():
         return _HERE
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"stream: expected a stream of cuda:{dev}, got one of cuda:{stream.device_index}")
     return _There(dev, stream, tensors)
 
 

@@ -255,10 +255,11 @@ int tpconv_double_backward(const tpconv_plan* plan, int64_t N, int64_t E, const 
  * linear map and the layer norm of irreps features.  Features and conventions
  * are those at the top of this file (fp32, contiguous, [mul][2l+1] blocks,
  * caller-owned memory, asynchronous on the stream, outputs overwritten).
- * They need no one-time device set-up: their first call may be a captured one.  No output may overlap an input or another output
- * (TPCONV_ERR_INVALID_ARG).  The pages define none of them: they are additions
- * of this library (what a layer of such a network holds next to the
- * convolution), with formulas of their own below.
+ * They need no one-time device set-up: their first call may be a captured one.
+ * No output may overlap an input or another output (TPCONV_ERR_INVALID_ARG).
+ * The pages define none of them: they are additions of this library (what a
+ * layer of such a network holds next to the convolution), with formulas of
+ * their own below.
  * ------------------------------------------------------------------------- */
 
 /* ---- nodes grouped by type ------------------------------------------------

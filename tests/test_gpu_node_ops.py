@@ -607,3 +607,36 @@ def test_gradients_together_and_one_by_one(T, n):
         assert len(r) == len(want[i % 3])
         for u, z in zip(r, want[i % 3]):
             assert torch.equal(u, z)
+
+
+def test_rows_beyond_32_bits(T):
+    """More than 2^31 floats in a tensor: only the last rows hold anything, and they and the weight gradients come
+    out as for those rows alone (norm: bit for bit; linear: another kernel, 2 TOL of the largest value)."""
+    import torch
+    irr, n, k = "64x0e+64x1o+64x2e", 3800011, 300
+    dim = 576
+    assert n * dim > 2 ** 31
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    r = rng(8)
+    few = {s: dev(f32(r.normal(size=(k, dim)))) for s in "xg"}
+    t = torch.arange(n, dtype=torch.int32, device="cuda") % 4
+    t[-k:] = dev(r.integers(-1, 4, k), torch.int32)
+    p, q = T.LinearPlan(irr, irr, n_types=4), T.NormPlan(irr)
+    w = dev(f32(r.normal(size=(4, p.weight_numel))))
+    G, H = T.NodeGroups(t, 4), T.NodeGroups(t[-k:], 4)
+    x, g = torch.zeros(n, dim, device="cuda"), torch.zeros(n, dim, device="cuda")
+    x[-k:], g[-k:] = few["x"], few["g"]
+    assert torch.equal(T.norm_forward(q, x)[-k:], T.norm_forward(q, few["x"]))
+    assert torch.equal(T.norm_backward(q, x, None, g, want=("dx",))["dx"][-k:],
+                       T.norm_backward(q, few["x"], None, few["g"], want=("dx",))["dx"])
+
+    def close(a, b):
+        assert (a - b).abs().max() <= 2 * TOL * b.abs().max()
+
+    close(T.linear_forward(p, G, x, w)[-k:], T.linear_forward(p, H, few["x"], w))
+    a, b = T.linear_backward(p, G, x, w, g), T.linear_backward(p, H, few["x"], w, few["g"])
+    close(a["dx"][-k:], b["dx"])
+    close(a["dweight"], b["dweight"])
+    assert not a["dx"][:-k].any()
+    torch.cuda.empty_cache()

@@ -183,3 +183,12 @@ def test_python_layer_refuses_host_tensors(T):
         T.NodeGroups(torch.zeros(3, dtype=torch.int32), 2)
     with pytest.raises(TypeError):
         T.linear_forward(T.LinearPlan("4x0e", "4x0e"), None, torch.zeros(3, 4), torch.zeros(1, 16))
+
+
+def test_streams_of_another_device_are_refused():
+    """(a stand-in for the stream: the check is the host's)"""
+    from types import SimpleNamespace
+    from equivariant_gnn_tensor_receiver_b200 import node
+    with pytest.raises(ValueError, match="stream"):
+        node._on(0, SimpleNamespace(device_index=1, cuda_stream=0))
+    assert isinstance(node._on(1, SimpleNamespace(device_index=1, cuda_stream=0)), node._There)
