@@ -29,7 +29,8 @@
 // (2048 floats) forward 312 us (floor 301), backward 548 (451), double backward 843 (752);
 // 32x l<=2 (288 floats) 53 (42), 92 (63), 142 (106).  Blocks that do not start on 16 bytes
 // (37x0e+21x1o+5x2e+3x0o, 128 floats, read 4 bytes at a time) 42 (19), 66 (28), 115 (47):
-// there the loads in flight bound it, not HBM.
+// there the instructions bound it (70 % of the issue slots; addresses, predicates and
+// the sums' shuffles for four bytes at a time), not HBM.
 #include <cuda_runtime.h>
 
 #include <algorithm>
