@@ -40,7 +40,7 @@ __device__ __forceinline__ void find_tile(const int* offsets, int T, int64_t N, 
     const int k = t0 + lane;
     int b = 0, e = 0;
     if (k < groups) lin_group(offsets, T, N, k, &b, &e);
-    const int n = (e - b + unit - 1) / unit;
+    const int n = units_of(e - b, unit);
     int s = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(256) k_linear_grad_reduce(const __grid_constan
     for (int k = threadIdx.x; k <= t; k += 32) {
       int b, e;
       lin_group(P.offsets, P.T, P.N, k, &b, &e);
-      const int c = (e - b + unit - 1) / unit;
+      const int c = units_of(e - b, unit);
       if (k < t) before += c;
       else n = c;
     }

@@ -55,6 +55,12 @@ struct LinGrad {
   LinPath p[kLinPaths];
 };
 
+// Tiles of `unit` nodes that n nodes make.  (n + unit - 1 would pass 2^31 for the largest graphs.)
+__host__ __device__ constexpr int units_of(int n, int unit) { return n > 0 ? (n - 1) / unit + 1 : 0; }
+static_assert(units_of(0x7fffffff, 120) == 17895698 && units_of(0x7fffffff, 0x7fffffff) == 1 && units_of(0, 9) == 0 &&
+                  units_of(-5, 9) == 0 && units_of(9, 9) == 1 && units_of(10, 9) == 2,
+              "N goes up to 2^31 - 1");
+
 // the nodes [b, e) of group t in perm; t == T is the group without a type
 __device__ __forceinline__ void lin_group(const int* offsets, int T, int64_t N, int t, int* b, int* e) {
   const int n = int(N);

@@ -109,7 +109,8 @@ __device__ __forceinline__ int total_cost(const Params& P, const int* total) {
 
 // a run of chunks of one type in one entry
 struct Piece {
-  int e, t, first, nodes;
+  int e, t, first;
+  unsigned nodes;  // (unsigned, as is all that steps past the last node: N may be 2^31 - 1)
   int slot;  // partial tile, or -1: the type's rows are all here
 };
 
@@ -123,7 +124,7 @@ struct Walk {
     const Run r = next_run(w, cuts, n, total, offs, T);
     if (r.e < 0) return false;
     const bool begins = r.first == offs[r.t], ends = r.end == offs[r.t + 1];
-    q->e = r.e, q->t = r.t, q->first = r.first, q->nodes = r.end - r.first;
+    q->e = r.e, q->t = r.t, q->first = r.first, q->nodes = unsigned(r.end - r.first);
     q->slot = begins && ends ? -1 : 2 * int(blockIdx.x) + begins;
     return true;
   }
@@ -261,9 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(&q)) {
       const Entry& L = E[q.e];
       const int d = L.d, cu = L.cu, cw = L.cw, nq = chunk_nodes(d);
-      for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
+      for (unsigned n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
         if ((ci & 1) != set) continue;
-        const int st = ci % stages, ab = set, kv = min(nq, q.nodes - n0) * d;
+        const int st = ci % stages, ab = set, kv = min(nq, int(q.nodes - n0)) * d;
         if (ci >= 2 && !wait(&sh.aempty[ab], ((ci >> 1) + 1) & 1, limit, abort, 1)) ok = false;
         if (ok && !wait(&sh.full[st], (ci / stages) & 1, limit, abort, 2)) ok = false;
         if (!ok) break;
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(&q)) {
       const Entry& L = E[q.e];
       const int cu = L.cu, cw = L.cw, nq = chunk_nodes(L.d);
-      const int rounds = ((q.nodes + nq - 1) / nq + kRound - 1) / kRound;
+      const int rounds = (units_of(int(q.nodes), nq) + kRound - 1) / kRound;
       const bool mine = (warp & 3) * 32 < cu && c0 < cw;
       float acc[32];
 #pragma unroll
@@ -366,14 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* src = is_g ? P.g + L.goff : P.x + L.xoff;
         const int dim = is_g ? P.dim_g : P.dim_x;
         const uint32_t bytes = uint32_t(is_g ? lg : lx) * 4;
-        auto node_of = [&](int k) {
+        auto node_of = [&](unsigned k) {
           const int n = k < q.nodes ? P.perm[q.first + k] : 0;
           return n >= 0 && n < P.N ? n : 0;
         };
         const int k = i0 / 2;
         int node = k < nq ? node_of(k) : 0;  // of the next chunk, read while this one is copied
-        for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-          const int st = ci % stages, cnt = min(nq, q.nodes - n0);
+        for (unsigned n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
+          const int st = ci % stages, cnt = min(nq, int(q.nodes - n0));
           const float* from = src + int64_t(node) * dim;
           if (k < nq && n0 + nq < q.nodes) node = node_of(n0 + nq + k);
           if (r < 2) prefetch_nodes(P.perm, q.first + n0 + kPermAhead + 32 * r, P.N);
@@ -395,9 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int d = L.d, nq = chunk_nodes(d), lx = L.cu * d, lg = L.cw * d;
         const float *x = P.x + L.xoff, *g = P.g + L.goff;
         // the nodes of the next chunk are read while this one is copied
-        int node = r < min(nq, q.nodes) ? P.perm[q.first + r] : 0;
-        for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-          const int st = ci % stages, cnt = min(nq, q.nodes - n0);
+        int node = r < min(nq, int(q.nodes)) ? P.perm[q.first + r] : 0;
+        for (unsigned n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
+          const int st = ci % stages, cnt = min(nq, int(q.nodes - n0));
           int* nodes = sh.node[ci & 1];
           if (r < 64) nodes[r] = (node >= 0 && node < P.N) ? node : 0;
           asm volatile("bar.sync 1, 192;" ::: "memory");
@@ -428,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n16 = (L.cw + 15) & ~15;
       const uint32_t id1 = idesc_tf32(kMT, SPLIT ? 2 * n16 : n16), id2 = idesc_tf32(kMT, n16);
       int in_round = 0;
-      for (int n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-        const int ab = ci & 1, db = ri & 1, steps = (min(nq, q.nodes - n0) * d + 7) / 8;
+      for (unsigned n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
+        const int ab = ci & 1, db = ri & 1, steps = (min(nq, int(q.nodes - n0)) * d + 7) / 8;
         if (in_round == 0 && ri >= 2 && !wait(&sh.dempty[db], ((ri >> 1) + 1) & 1, limit, abort, 5)) ok = false;
         if (ok && !wait(&sh.afull[ab], (ci >> 1) & 1, limit, abort, 6)) ok = false;
         if (!ok) break;

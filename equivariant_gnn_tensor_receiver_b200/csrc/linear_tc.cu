@@ -153,7 +153,7 @@ struct Walk {
     it->count = min(unit, end - at);
     it->run = fresh;
     it->zero = zero;
-    at += unit;
+    at += it->count;
     it->run_last = at >= end;
     return true;
   }
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!P.accumulate) {
       const int b = offs[P.T], nz = max(int(P.N) - b, 0);
       const int z0 = b + share_begin(nz, blockIdx.x, gridDim.x), z1 = b + share_begin(nz, blockIdx.x + 1, gridDim.x);
-      for (int i = z0 + (warp - 8); i < z1; i += 8) {
+      for (unsigned i = z0 + (warp - 8); i < unsigned(z1); i += 8) {  // (i passes 2^31 behind the largest graphs)
         const int n = P.perm[i];
         if (n < 0 || n >= P.N) continue;
         float* dst = P.out + int64_t(n) * P.dim_out;
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         more = next_item(&it);
         if (more) {
           node = node_of(it);  // read while this tile is copied
-          if (r < 4) prefetch_nodes(P.perm, it.first + kPermAhead + 32 * r, P.N);
+          if (r < 4) prefetch_nodes(P.perm, unsigned(it.first) + kPermAhead + 32 * r, P.N);
         }
         const uint32_t mine = cur.count > w ? uint32_t(cur.count - w + kCopyWarps - 1) / kCopyWarps : 0;
         for (int s = 0; ok && s < O.count; ++s) {
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         more = next_item(&it);
         if (more) {
           node = node_of(it);  // read while this tile is copied
-          if (r < 4) prefetch_nodes(P.perm, it.first + kPermAhead + 32 * r, P.N);
+          if (r < 4) prefetch_nodes(P.perm, unsigned(it.first) + kPermAhead + 32 * r, P.N);
         }
         asm volatile("bar.sync 3, 160;" ::: "memory");
         for (int s = 0; ok && s < O.count; ++s) {

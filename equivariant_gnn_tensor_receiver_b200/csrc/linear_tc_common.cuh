@@ -62,8 +62,8 @@ __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_
 // Brings the node ids some tiles ahead into L2: a tile's copies are issued in less time than
 // HBM answers, so that reading the ids one tile ahead alone would bound them.
 constexpr int kPermAhead = 512;
-__device__ __forceinline__ void prefetch_nodes(const int* perm, int at, int64_t N) {
-  if (at >= 0 && at < N) asm volatile("prefetch.global.L2 [%0];" ::"l"(perm + at));
+__device__ __forceinline__ void prefetch_nodes(const int* perm, unsigned at, int64_t N) {
+  if (at < N) asm volatile("prefetch.global.L2 [%0];" ::"l"(perm + at));
 }
 
 // untiled bulk copies: both addresses and the size are multiples of 16 bytes
@@ -163,8 +163,7 @@ __device__ __forceinline__ void load_offsets(int* offs, const int* offsets, int 
     offs[t] = t <= T ? min(max(offsets[t], 0), int(N)) : int(N);
 }
 __device__ __forceinline__ int group_units(const int* offs, int t, int unit) {
-  const int n = offs[t + 1] - offs[t];
-  return n > 0 ? (n + unit - 1) / unit : 0;
+  return units_of(offs[t + 1] - offs[t], unit);
 }
 // units of the first `groups` groups; one warp, the same answer in every lane
 __device__ __forceinline__ int count_units(const int* offs, int groups, int unit) {
@@ -265,9 +264,10 @@ static __device__ __noinline__ Run next_run(WalkState* w, const Cut* cuts, int n
   }
   Run r{-1, 0, 0, 0};
   if (s.t < T) {
-    const int end = offs[s.t + 1], take = min((end - s.at + nodes - 1) / nodes, s.left);
-    r = {s.e, s.t, s.at, end - s.at <= take * nodes ? end : s.at + take * nodes};
-    s.left -= take;
+    const int end = offs[s.t + 1], all = units_of(end - s.at, nodes);
+    const bool whole = all <= s.left;  // (the whole tiles alone end below 2^31)
+    r = {s.e, s.t, s.at, whole ? end : s.at + s.left * nodes};
+    s.left -= whole ? all : s.left;
   }
   if ((threadIdx.x & 31) == 0) *w = s;
   __syncwarp();
