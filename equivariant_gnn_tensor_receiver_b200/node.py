@@ -66,7 +66,7 @@ class _Here:
 
 class _There:
     """The device current and, with an explicit stream, that stream too: what is allocated inside belongs to it,
-    and the inputs are not reused before its work on them is done."""
+    and what the caller brings (inputs, ``out``, ``ws``) is not reused before its work on them is done."""
 
     def __init__(self, dev, stream, tensors):
         self.dev, self.stream, self.tensors = torch.cuda.device(dev), stream, tensors
@@ -81,7 +81,7 @@ class _There:
         if self.stream is not None:
             self.outer.__exit__(*e)
             for t in self.tensors:
-                if t is not None and t.numel():
+                if isinstance(t, torch.Tensor) and t.is_cuda and t.numel():  # (a refused one may be anything)
                     t.record_stream(self.stream)
         self.dev.__exit__(*e)
 
@@ -169,7 +169,7 @@ def linear_forward(plan, groups, x, weight, out=None, ws=None, stream=None):
     """out[N, dim_out]: every node's features times the weight of its type; rows of no group are zero."""
     N, dev, rin, rout, w = _groups(plan, groups)
     px, pw = _ptr("x", x, rin, dev), _ptr("weight", weight, w, dev)
-    with _on(dev, stream, x, weight, groups.perm, groups.offsets):
+    with _on(dev, stream, x, weight, groups.perm, groups.offsets, out, ws):
         if out is None:
             out, po = _new(x, True, *rout)
         else:
@@ -185,7 +185,7 @@ def linear_backward(plan, groups, x, weight, g, want=("dx", "dweight"), ws=None,
     N, dev, rin, rout, w = _groups(plan, groups)
     px, pw, pg = _ptr("x", x, rin, dev), _ptr("weight", weight, w, dev), _ptr("g", g, rout, dev)
     _wanted(want, ("dx", "dweight"))
-    with _on(dev, stream, x, weight, g, groups.perm, groups.offsets):
+    with _on(dev, stream, x, weight, g, groups.perm, groups.offsets, ws):
         dx, pdx = _new(x, "dx" in want, *rin)
         dw, pdw = _new(x, "dweight" in want, *w)
         _ws, wp, wn = _workspace(ws, plan.workspace_bytes(L.OP_BACKWARD, N), x)
@@ -201,7 +201,7 @@ def linear_double_backward(plan, groups, x, weight, g, gg_x=None, gg_weight=None
     px, pw, pg = _ptr("x", x, rin, dev), _ptr("weight", weight, w, dev), _ptr("g", g, rout, dev)
     pa, pal = _ptr("gg_x", gg_x, rin, dev, True), _ptr("gg_weight", gg_weight, w, dev, True)
     _wanted(want, ("d_g", "d_x", "d_weight"))
-    with _on(dev, stream, x, weight, g, gg_x, gg_weight, groups.perm, groups.offsets):
+    with _on(dev, stream, x, weight, g, gg_x, gg_weight, groups.perm, groups.offsets, ws):
         d_g, pdg = _new(x, "d_g" in want, *rout)
         d_x, pdx = _new(x, "d_x" in want, *rin)
         d_w, pdw = _new(x, "d_weight" in want, *w)
@@ -228,7 +228,7 @@ def norm_forward(plan, x, weight=None, bias=None, out=None, stream=None):
     N, dev, rows, px = _rows(plan, x)
     pw = _ptr("weight", weight, (plan.weight_numel,), dev, True)
     pb = _ptr("bias", bias, (plan.bias_numel,), dev, True)
-    with _on(dev, stream, x, weight, bias):
+    with _on(dev, stream, x, weight, bias, out):
         if out is None:
             out, po = _new(x, True, *rows)
         else:
@@ -242,7 +242,7 @@ def norm_backward(plan, x, weight, g, want=("dx", "dweight", "dbias"), ws=None, 
     N, dev, rows, px = _rows(plan, x)
     pw, pg = _ptr("weight", weight, (plan.weight_numel,), dev, True), _ptr("g", g, rows, dev)
     _wanted(want, ("dx", "dweight", "dbias"))
-    with _on(dev, stream, x, weight, g):
+    with _on(dev, stream, x, weight, g, ws):
         dx, pdx = _new(x, "dx" in want, *rows)
         dw, pdw = _new(x, "dweight" in want, plan.weight_numel)
         db, pdb = _new(x, "dbias" in want, plan.bias_numel)
@@ -260,7 +260,7 @@ def norm_double_backward(plan, x, weight, g, gg_x=None, gg_weight=None, gg_bias=
     pa, pal = _ptr("gg_x", gg_x, rows, dev, True), _ptr("gg_weight", gg_weight, nw, dev, True)
     pbe = _ptr("gg_bias", gg_bias, (plan.bias_numel,), dev, True)
     _wanted(want, ("d_g", "d_x", "d_weight"))
-    with _on(dev, stream, x, weight, g, gg_x, gg_weight, gg_bias):
+    with _on(dev, stream, x, weight, g, gg_x, gg_weight, gg_bias, ws):
         d_g, pdg = _new(x, "d_g" in want, *rows)
         d_x, pdx = _new(x, "d_x" in want, *rows)
         d_w, pdw = _new(x, "d_weight" in want, plan.weight_numel)

@@ -52,3 +52,64 @@ def test_linear_of_the_most_nodes(T, gemm):
     assert T._lib.tpconv_linear_device_status(p) == 0
     del x, g, out, dx, r, G, types
     torch.cuda.empty_cache()
+
+
+def calls_with_buffers(T):
+    """name, call(ws or out, stream), elements and type of the caller's buffer"""
+    import torch
+    n, irr = 600, "64x0e+32x1o"
+    dim = 160
+    p, q = T.LinearPlan(irr, irr, n_types=3), T.NormPlan(irr)
+    G = T.NodeGroups(torch.arange(n, dtype=torch.int32, device="cuda") % 3, 3)
+    x, g, a = (torch.randn(n, dim, device="cuda") for _ in range(3))
+    w = torch.randn(3, p.weight_numel, device="cuda")
+    kb = lambda plan, op: (plan.workspace_bytes(op, n), torch.uint8)  # noqa: E731
+    rows = (n * dim, torch.float32)
+    return [
+        ("linear_forward out", lambda b, s: T.linear_forward(p, G, x, w, out=b.view(n, dim), stream=s), rows),
+        ("linear_forward ws", lambda b, s: T.linear_forward(p, G, x, w, ws=b, stream=s), (1 << 20, torch.uint8)),
+        ("linear_backward ws", lambda b, s: T.linear_backward(p, G, x, w, g, ws=b, stream=s), kb(p, 1)),
+        ("linear_double_backward ws", lambda b, s: T.linear_double_backward(p, G, x, w, g, a, w, ws=b, stream=s),
+         kb(p, 2)),
+        ("norm_forward out", lambda b, s: T.norm_forward(q, x, out=b.view(n, dim), stream=s), rows),
+        ("norm_backward ws", lambda b, s: T.norm_backward(q, x, None, g, ws=b, stream=s), kb(q, 1)),
+        ("norm_double_backward ws", lambda b, s: T.norm_double_backward(q, x, None, g, a, ws=b, stream=s), kb(q, 2)),
+    ]
+
+
+def test_buffers_of_the_caller_are_held_for_the_stream(T):
+    """A caller drops ``out`` or ``ws`` right after a call on another stream that is still busy: the allocator does
+    not hand the memory to the current stream before the call is done."""
+    import torch
+    side = torch.cuda.Stream()
+    for name, call, (numel, dtype) in calls_with_buffers(T):
+        new = lambda: torch.empty(numel, dtype=dtype, device="cuda")  # noqa: E731
+        call(new(), side)  # (the first call loads its kernels, which waits for the device)
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        b = new()
+        at = b.data_ptr()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # some 0.1 s of work ahead of the call
+        call(b, side)
+        busy = not side.query()
+        del b
+        other = new()
+        assert busy and other.data_ptr() != at, name
+        side.synchronize()
+
+
+def test_refused_buffers_on_a_stream(T):
+    """what is wrong with ``out`` or ``ws`` is said as without a stream, and the current device and stream stay"""
+    import torch
+    side = torch.cuda.Stream()
+    x = torch.zeros(4, 8, device="cuda")
+    q = T.NormPlan("8x0e")
+    here = torch.cuda.current_stream()
+    for bad, error in ((3, TypeError), (torch.zeros(1 << 16, dtype=torch.uint8), ValueError)):
+        with pytest.raises(error):
+            T.norm_backward(q, x, None, x.clone(), ws=bad, stream=side)
+    for bad, error in ((3, TypeError), (torch.zeros(4, 8), ValueError), (x[:3], ValueError)):
+        with pytest.raises(error):
+            T.norm_forward(q, x, out=bad, stream=side)
+    assert torch.cuda.current_stream() == here and torch.cuda.current_device() == 0
