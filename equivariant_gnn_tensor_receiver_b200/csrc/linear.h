@@ -55,10 +55,12 @@ struct LinGrad {
   LinPath p[kLinPaths];
 };
 
-// Tiles of `unit` nodes that n nodes make.  (n + unit - 1 would pass 2^31 for the largest graphs.)
-__host__ __device__ constexpr int units_of(int n, int unit) { return n > 0 ? (n - 1) / unit + 1 : 0; }
+// Tiles of `unit` nodes that n >= 0 nodes make.  (Unsigned: n + unit - 1 passes 2^31 for the largest graphs.)
+__host__ __device__ constexpr int units_of(int n, int unit) {
+  return int((unsigned(n) + unsigned(unit) - 1) / unsigned(unit));
+}
 static_assert(units_of(0x7fffffff, 120) == 17895698 && units_of(0x7fffffff, 0x7fffffff) == 1 && units_of(0, 9) == 0 &&
-                  units_of(-5, 9) == 0 && units_of(9, 9) == 1 && units_of(10, 9) == 2,
+                  units_of(9, 9) == 1 && units_of(10, 9) == 2,
               "N goes up to 2^31 - 1");
 
 // the nodes [b, e) of group t in perm; t == T is the group without a type

@@ -109,8 +109,7 @@ __device__ __forceinline__ int total_cost(const Params& P, const int* total) {
 
 // a run of chunks of one type in one entry
 struct Piece {
-  int e, t, first;
-  unsigned nodes;  // (unsigned, as is all that steps past the last node: N may be 2^31 - 1)
+  int e, t, end, nodes;  // (counted down to `end`: a step past it would pass 2^31 in the largest graphs)
   int slot;  // partial tile, or -1: the type's rows are all here
 };
 
@@ -124,7 +123,7 @@ struct Walk {
     const Run r = next_run(w, cuts, n, total, offs, T);
     if (r.e < 0) return false;
     const bool begins = r.first == offs[r.t], ends = r.end == offs[r.t + 1];
-    q->e = r.e, q->t = r.t, q->first = r.first, q->nodes = unsigned(r.end - r.first);
+    q->e = r.e, q->t = r.t, q->end = r.end, q->nodes = r.end - r.first;
     q->slot = begins && ends ? -1 : 2 * int(blockIdx.x) + begins;
     return true;
   }
@@ -262,9 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(&q)) {
       const Entry& L = E[q.e];
       const int d = L.d, cu = L.cu, cw = L.cw, nq = chunk_nodes(d);
-      for (unsigned n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
+      const int end = ci + units_of(q.nodes, nq), tail = (q.nodes - (end - ci - 1) * nq) * d;  // rows of the last
+      for (; ci < end; ++ci) {
         if ((ci & 1) != set) continue;
-        const int st = ci % stages, ab = set, kv = min(nq, int(q.nodes - n0)) * d;
+        const int st = ci % stages, ab = set, kv = ci + 1 < end ? nq * d : tail;
         if (ci >= 2 && !wait(&sh.aempty[ab], ((ci >> 1) + 1) & 1, limit, abort, 1)) ok = false;
         if (ok && !wait(&sh.full[st], (ci / stages) & 1, limit, abort, 2)) ok = false;
         if (!ok) break;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(&q)) {
       const Entry& L = E[q.e];
       const int cu = L.cu, cw = L.cw, nq = chunk_nodes(L.d);
-      const int rounds = (units_of(int(q.nodes), nq) + kRound - 1) / kRound;
+      const int rounds = (units_of(q.nodes, nq) + kRound - 1) / kRound;
       const bool mine = (warp & 3) * 32 < cu && c0 < cw;
       float acc[32];
 #pragma unroll
@@ -367,17 +367,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* src = is_g ? P.g + L.goff : P.x + L.xoff;
         const int dim = is_g ? P.dim_g : P.dim_x;
         const uint32_t bytes = uint32_t(is_g ? lg : lx) * 4;
-        auto node_of = [&](unsigned k) {
-          const int n = k < q.nodes ? P.perm[q.first + k] : 0;
+        auto node_of = [&](int k, int left) {  // of a chunk, from which on `left` nodes are left
+          const int n = k < left ? P.perm[q.end - left + k] : 0;
           return n >= 0 && n < P.N ? n : 0;
         };
         const int k = i0 / 2;
-        int node = k < nq ? node_of(k) : 0;  // of the next chunk, read while this one is copied
-        for (unsigned n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-          const int st = ci % stages, cnt = min(nq, int(q.nodes - n0));
+        int node = k < nq ? node_of(k, q.nodes) : 0;  // of the next chunk, read while this one is copied
+        for (int left = q.nodes; left > 0; left -= nq, ++ci) {
+          const int st = ci % stages, cnt = min(nq, left);
           const float* from = src + int64_t(node) * dim;
-          if (k < nq && n0 + nq < q.nodes) node = node_of(n0 + nq + k);
-          if (r < 2) prefetch_nodes(P.perm, q.first + n0 + kPermAhead + 32 * r, P.N);
+          if (k < nq && left > nq) node = node_of(k, left - nq);
+          if (r < 2) prefetch_nodes(P.perm, unsigned(q.end - left) + kPermAhead + 32 * r, P.N);
           const uint32_t mine = __reduce_add_sync(0xffffffffu, k < cnt ? bytes : 0u);
           if (ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
           if (!ok) break;
@@ -396,14 +396,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int d = L.d, nq = chunk_nodes(d), lx = L.cu * d, lg = L.cw * d;
         const float *x = P.x + L.xoff, *g = P.g + L.goff;
         // the nodes of the next chunk are read while this one is copied
-        int node = r < min(nq, int(q.nodes)) ? P.perm[q.first + r] : 0;
-        for (unsigned n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-          const int st = ci % stages, cnt = min(nq, int(q.nodes - n0));
+        int node = r < min(nq, q.nodes) ? P.perm[q.end - q.nodes + r] : 0;
+        for (int left = q.nodes; left > 0; left -= nq, ++ci) {
+          const int st = ci % stages, cnt = min(nq, left);
           int* nodes = sh.node[ci & 1];
           if (r < 64) nodes[r] = (node >= 0 && node < P.N) ? node : 0;
           asm volatile("bar.sync 1, 192;" ::: "memory");
-          node = r < nq && n0 + nq + r < q.nodes ? P.perm[q.first + n0 + nq + r] : 0;
-          if (r < 2) prefetch_nodes(P.perm, q.first + n0 + kPermAhead + 32 * r, P.N);
+          node = r < nq && r < left - nq ? P.perm[q.end - left + nq + r] : 0;
+          if (r < 2) prefetch_nodes(P.perm, unsigned(q.end - left) + kPermAhead + 32 * r, P.N);
           if (ok && ci >= stages && !wait(&sh.empty[st], ((ci / stages) + 1) & 1, limit, abort, 4)) ok = false;
           if (!ok) continue;
           const uint32_t dst = smem_u32(sRaw + st * stage_bytes);
@@ -429,13 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n16 = (L.cw + 15) & ~15;
       const uint32_t id1 = idesc_tf32(kMT, SPLIT ? 2 * n16 : n16), id2 = idesc_tf32(kMT, n16);
       int in_round = 0;
-      for (unsigned n0 = 0; n0 < q.nodes; n0 += nq, ++ci) {
-        const int ab = ci & 1, db = ri & 1, steps = (min(nq, int(q.nodes - n0)) * d + 7) / 8;
+      for (int left = q.nodes; left > 0; left -= nq, ++ci) {
+        const int ab = ci & 1, db = ri & 1, steps = (min(nq, left) * d + 7) / 8;
         if (in_round == 0 && ri >= 2 && !wait(&sh.dempty[db], ((ri >> 1) + 1) & 1, limit, abort, 5)) ok = false;
         if (ok && !wait(&sh.afull[ab], (ci >> 1) & 1, limit, abort, 6)) ok = false;
         if (!ok) break;
         fence_after_sync();
-        const bool last = ++in_round == kRound || n0 + nq >= q.nodes;
+        const bool last = ++in_round == kRound || left <= nq;
         if (lane == 0) {
           const uint32_t td = tmem + kTmemD + db * kTmemDStage, a = tmem + kTmemA + ab * kTmemAStage;
           const uint64_t b = sw128_kmajor(smem_u32(sB + ab * kBTile));

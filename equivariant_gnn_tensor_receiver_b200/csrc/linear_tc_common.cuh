@@ -163,7 +163,8 @@ __device__ __forceinline__ void load_offsets(int* offs, const int* offsets, int 
     offs[t] = t <= T ? min(max(offsets[t], 0), int(N)) : int(N);
 }
 __device__ __forceinline__ int group_units(const int* offs, int t, int unit) {
-  return units_of(offs[t + 1] - offs[t], unit);
+  const int n = offs[t + 1] - offs[t];
+  return n > 0 ? units_of(n, unit) : 0;
 }
 // units of the first `groups` groups; one warp, the same answer in every lane
 __device__ __forceinline__ int count_units(const int* offs, int groups, int unit) {
