@@ -141,6 +141,16 @@ __global__ void __launch_bounds__(256) k_linear_rows(const __grid_constant__ Lin
 // The nodes of a type are cut into pieces of `unit`; CTA (piece, path tile) adds the
 // piece's rows into a 64 x 64 tile and stores it as the piece's partial.  The reduce
 // kernel adds a type's pieces in order.
+// A piece of a wide plan, or of a plan of few tiles, has any number of rows, and one FP32
+// chain over them loses 1.5e-5 of the sum at 262144 rows.  So a chain ends after kChain rows
+// and is added to the piece's partial, which is this CTA's alone: roundings of 256 + rows / 256
+// additions in a row, 1e-6 at 262144 rows.  Measured (dweight, device; in brackets one chain):
+// 8192 nodes of 512x l <= 2 2.22 ms (2.25), 65536 of 64x l <= 2 750 us (722), 100000 of 1024x0e
+// 17.7 ms (14.2: 48 registers hold five CTAs on an SM, 40 held six, and its 768 CTAs in one
+// wave).  The second sums in registers: 80 of them, 2.79 ms for the first; in shared memory,
+// with their errors carried along: 2.40 ms.
+constexpr int kChain = 256;
+static_assert(kChain % kTK == 0, "whole steps");
 __global__ void __launch_bounds__(256) k_linear_grad(const __grid_constant__ LinGrad P, int unit, int tiles_u,
                                                      int tiles_w, float* __restrict__ part) {
   __shared__ float sa[kTK][kTR + 4], sb[kTK][kTC + 4];
@@ -161,6 +171,7 @@ __global__ void __launch_bounds__(256) k_linear_grad(const __grid_constant__ Lin
   const int d = Q.d, rows = count * d;
   float acc[4][4] = {};
   const int tr = (threadIdx.x / 16) * 4, tc = (threadIdx.x % 16) * 4;
+  float* o = part + int64_t(blockIdx.x) * P.wnumel + Q.woff;
   for (int r0 = 0; r0 < rows; r0 += kTK) {
     for (int i = threadIdx.x; i < kTK * kTR; i += 256) {
       const int k = i / kTR, c = i % kTR, r = r0 + k;
@@ -187,13 +198,20 @@ __global__ void __launch_bounds__(256) k_linear_grad(const __grid_constant__ Lin
         for (int j = 0; j < 4; ++j) acc[i][j] += a[i] * b[j];
     }
     __syncthreads();
+    if ((r0 + kTK) % kChain != 0 && r0 + kTK < rows) continue;
+    int co = Q.co;
+    asm volatile("" : "+r"(co));  // (or 16 addresses are kept through the loop: 62 registers, not 48)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (u0 + tr + i < Q.ci && w0 + tc + j < co) {
+          float* to = o + int64_t(u0 + tr + i) * co + w0 + tc + j;
+          *to = r0 >= kChain ? *to + acc[i][j] : acc[i][j];
+        }
+        acc[i][j] = 0.f;
+      }
   }
-  float* o = part + int64_t(blockIdx.x) * P.wnumel + Q.woff;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (u0 + tr + i < Q.ci && w0 + tc + j < Q.co) o[int64_t(u0 + tr + i) * Q.co + w0 + tc + j] = acc[i][j];
 }
 
 // dW[t][i] = sum of part[piece][i] over the pieces of type t = blockIdx.y, in order

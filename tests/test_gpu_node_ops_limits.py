@@ -113,3 +113,46 @@ def test_refused_buffers_on_a_stream(T):
         with pytest.raises(error):
             T.norm_forward(q, x, out=bad, stream=side)
     assert torch.cuda.current_stream() == here and torch.cuda.current_device() == 0
+
+
+@pytest.mark.parametrize("i,o,gemm", [("1024x0e", "704x0e", "fp32"), ("512x1o", "512x1o", "simt")])
+def test_linear_weight_gradient_of_many_rows(T, i, o, gemm):
+    """The FP32 kernel (wide plans take it in every mode) over up to 240 000 nodes of one type, 64-bit sums beside it.
+    Terms of one sign, so nothing cancels.  Tolerance: chains of 256 additions, at most 938 of them added up (l = 1:
+    704 of three rows a node in four pieces), each with a rounding of at most 2^-24 of the sum, spread evenly: a
+    standard deviation under sqrt(256 + 938) 2^-24 / sqrt(3) = 1.2e-6 of it; 1e-5 is eight of those."""
+    import torch
+    n = 300_000
+    torch.manual_seed(3)
+    p = T.LinearPlan(i, o, n_types=3, gemm=gemm)
+    types = torch.randint(-1, 2, (n,), dtype=torch.int32, device="cuda")
+    types[:240_000] = 1
+    G = T.NodeGroups(types, 3)
+    x, g = torch.rand(n, p.dim_in, device="cuda").add_(0.5), torch.rand(n, p.dim_out, device="cuda").add_(0.5)
+    w = torch.zeros(3, p.weight_numel, device="cuda")
+    dw = T.linear_backward(p, G, x, w, g, want=("dweight",))["dweight"]
+    q = p.paths[0]
+    d = 2 * q["l"] + 1
+    for t in range(3):
+        want = torch.zeros(q["c_in"], q["c_out"], dtype=torch.float64, device="cuda")
+        for rows in torch.nonzero(types == t)[:, 0].split(20_000):
+            a, b = x[rows].double().view(-1, q["c_in"], d), g[rows].double().view(-1, q["c_out"], d)
+            want += a.transpose(1, 2).reshape(-1, q["c_in"]).t() @ b.transpose(1, 2).reshape(-1, q["c_out"])
+        assert ((dw[t].view_as(want).double() - want).abs() <= 1e-5 * want).all()
+    assert T._lib.tpconv_linear_device_status(p) == 0
+
+
+def test_linear_weight_gradient_keeps_infinities(T):
+    """gemm "simt": an infinity among thousands of rows of a type, and a sum that overflows, stay infinite"""
+    import torch
+    n = 20_000
+    torch.manual_seed(4)
+    p = T.LinearPlan("3x0e", "2x0e", gemm="simt")
+    G = T.NodeGroups(torch.zeros(n, dtype=torch.int32, device="cuda"), 1)
+    x, g = torch.rand(n, 3, device="cuda") + 0.5, torch.rand(n, 2, device="cuda") + 0.5
+    g[:, 1] *= -1
+    x[5, 0] = float("inf")
+    x[:, 1] = 3e38
+    dw = T.linear_backward(p, G, x, torch.zeros(1, 6, device="cuda"), g)["dweight"].view(3, 2)
+    inf = float("inf")
+    assert dw[:2].tolist() == [[inf, -inf], [inf, -inf]] and torch.isfinite(dw[2]).all()
