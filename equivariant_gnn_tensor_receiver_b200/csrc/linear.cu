@@ -40,7 +40,9 @@ __device__ __forceinline__ void find_tile(const int* offsets, int T, int64_t N, 
     const int k = t0 + lane;
     int b = 0, e = 0;
     if (k < groups) lin_group(offsets, T, N, k, &b, &e);
-    const int n = units_of(e - b, unit);
+    // (units_of, with a signed division: the rows kernel gets 48 registers by it and not 40, and takes
+    // 36 and not 40 us at 4096 nodes of 64x0e+64x1o+64x2e)
+    const int q = (e - b) / unit, n = q + (q * unit < e - b);
     int s = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
