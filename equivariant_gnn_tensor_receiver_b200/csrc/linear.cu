@@ -216,8 +216,9 @@ __global__ void __launch_bounds__(256) k_linear_grad(const __grid_constant__ Lin
   }
 }
 
-// dW[t][i] = sum of part[piece][i] over the pieces of type t = blockIdx.y, in order
-__global__ void __launch_bounds__(256) k_linear_grad_reduce(const __grid_constant__ LinGrad P, int unit,
+// dW[t][i] = sum of part[piece][i] over the pieces of type t = blockIdx.y, in order.  (Groups
+// that overlap, from offsets that do not ascend, would have more than the workspace's pieces.)
+__global__ void __launch_bounds__(256) k_linear_grad_reduce(const __grid_constant__ LinGrad P, int unit, int pieces,
                                                             const float* part) {
   __shared__ int s_lo, s_n;
   const int t = blockIdx.y;
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(256) k_linear_grad_reduce(const __grid_constan
     }
     before = __reduce_add_sync(0xffffffffu, before);
     n = __reduce_add_sync(0xffffffffu, n);
-    if (threadIdx.x == 0) s_lo = before, s_n = n;
+    if (threadIdx.x == 0) s_lo = min(before, pieces), s_n = min(n, pieces - s_lo);
   }
   __syncthreads();
   chain_wait();
@@ -391,7 +392,8 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
   if (e) return e;
   const unsigned bx = unsigned(std::min<int64_t>((p->wnumel + 255) / 256, 1024));
   ph.note(2);
-  return chain_launch(k_linear_grad_reduce, dim3(bx, unsigned(p->T)), 256, 0, st, G, unit, static_cast<const float*>(part));
+  return chain_launch(k_linear_grad_reduce, dim3(bx, unsigned(p->T)), 256, 0, st, G, unit, int(pieces),
+                      static_cast<const float*>(part));
 }
 
 size_t ws_bytes(const tpconv_linear* p, int op, int64_t N) {

@@ -503,7 +503,8 @@ __global__ void __launch_bounds__(256) k_linear_grad_join(const __grid_constant_
       // the shares that hold the first and the last chunk
       const int per = all / ctas, more = all - per * ctas, wide = more * (per + 1);
       auto owner = [&](int x) { return x < wide ? x / (per + 1) : more + (x - wide) / max(per, 1); };
-      const int first = owner(seg), last = owner(end);
+      // (within the CTAs whatever the offsets say: groups that overlap cost more than was planned for)
+      const int first = min(max(owner(seg), 0), ctas - 1), last = min(max(owner(end), 0), ctas - 1);
       m = 0;
       for (int b0 = first; b0 <= last; b0 += 32) {
         const int b = b0 + threadIdx.x;

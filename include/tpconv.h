@@ -283,7 +283,8 @@ int tpconv_group_nodes(int64_t N, int n_types, const int32_t* type, int32_t* per
  * d_g and d_x); they add nothing to dweight / d_weight.
  * perm / offsets come from tpconv_group_nodes for the same N and n_types.
  * (Entries outside [0, N] are never followed; the rows they stand for are
- * then undefined.)
+ * then undefined.  Offsets that do not ascend leave the results undefined, but
+ * nothing outside the tensors and the workspace is read or written.)
  *   gemm: TPCONV_GEMM_FP32 / _TF32 / _SIMT as in tpconv_options, for any
  *   multiplicities and alignment (blocks whose multiplicities are multiples of
  *   4 in 16-byte aligned tensors run fastest).  Small calls, and plans with more

@@ -156,3 +156,26 @@ def test_linear_weight_gradient_keeps_infinities(T):
     dw = T.linear_backward(p, G, x, torch.zeros(1, 6, device="cuda"), g)["dweight"].view(3, 2)
     inf = float("inf")
     assert dw[:2].tolist() == [[inf, -inf], [inf, -inf]] and torch.isfinite(dw[2]).all()
+
+
+@pytest.mark.parametrize("irr,n,gemm", [("8x0e", 300, "simt"), ("64x0e+64x1o", 3000, "fp32")])
+def test_linear_of_offsets_that_do_not_ascend(T, irr, n, gemm):
+    """groups that overlap: results are undefined, but nothing behind the workspace gets into them, and no wait
+    runs out"""
+    import torch
+    L = T._lib
+    p = T.LinearPlan(irr, irr, n_types=4, gemm=gemm)
+    perm = torch.arange(n, dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, n, 0, n, 0], dtype=torch.int32, device="cuda")
+    x, g = (torch.randn(n, p.dim_in, device="cuda") for _ in range(2))
+    w = torch.randn(4, p.weight_numel, device="cuda")
+    dx, dw = torch.zeros_like(x), torch.zeros_like(w)
+    need = p.workspace_bytes(T.OP_BACKWARD, n)
+    ws = torch.zeros(need // 4 + (1 << 22), device="cuda")
+    ws[need // 4:] = float("nan")
+    st = L.lib().tpconv_linear_backward(p.handle, n, perm.data_ptr(), offsets.data_ptr(), x.data_ptr(), w.data_ptr(),
+                                        g.data_ptr(), dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), need,
+                                        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and L.tpconv_linear_device_status(p) == 0
+    assert torch.isfinite(dw).all() and torch.isfinite(dx).all() and ws[need // 4:].isnan().all()
