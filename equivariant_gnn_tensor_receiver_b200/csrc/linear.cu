@@ -268,19 +268,22 @@ namespace {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// nodes of a piece of the weight gradient: enough pieces to fill the GPU about twice
-int grad_unit(const tpconv_linear* p, int64_t N) {
+// pieces of the FP32 weight gradient: enough to fill the GPU about twice; nodes of a piece
+int64_t grad_pieces(const tpconv_linear* p) {
   int cu = 1, cw = 1;
   for (int i = 0; i < p->n_paths; ++i) {
     cu = std::max(cu, ceil_div(p->path[i].ci, kTR));
     cw = std::max(cw, ceil_div(p->path[i].co, kTC));
   }
-  const int64_t want = std::max<int64_t>(1, 2 * kSMs / std::max(1, p->n_paths * cu * cw));
+  return std::max<int64_t>(1, 2 * kSMs / std::max(1, p->n_paths * cu * cw));
+}
+int grad_unit(const tpconv_linear* p, int64_t N) {
+  const int64_t want = grad_pieces(p);
   return int(std::max<int64_t>(16, (N + want - 1) / want));
 }
+// its partials for up to N nodes (tile_bound(n, T, grad_unit(p, n)) is within this for every n <= N)
 size_t grad_partials(const tpconv_linear* p, int64_t N) {
-  if (N == 0 || p->wnumel == 0) return 0;
-  return size_t(tile_bound(N, p->T, grad_unit(p, N))) * size_t(p->wnumel) * 4;
+  return size_t(std::min(N / 16, grad_pieces(p)) + std::min<int64_t>(p->T, N)) * size_t(p->wnumel) * 4;
 }
 
 // the row product of `transposed` (dx, d_x) or plain (out, d_g) blocks with one or two operand pairs
@@ -318,6 +321,16 @@ double mega_macs(const tpconv_linear* p, int64_t N) {
   double m = 0;
   for (int i = 0; i < p->n_paths; ++i) m += double(p->path[i].ci) * p->path[i].co * p->path[i].d;
   return m * 1e-6 * double(N);
+}
+
+// The weight gradient's small calls run on the FP32 pipes, as the rows' do.  Measured, FP32 /
+// tensor cores in us: 64x0e+64x1o+64x2e, 64 nodes 14.4 / 16.5, 512 nodes 18.5 / 19.1 (8 types)
+// and 18.5 / 22.6 (one); 128 channels up to l = 3, 32 nodes 16.5 / 18.5, 512 nodes 43 / 27.
+// Up to how many nodes a call is small:
+int64_t grad_small(const tpconv_linear* p) { return int64_t(std::min(512.0, 20 / std::max(mega_macs(p, 1), 1e-6))); }
+// whether a call's weight gradient runs on the tensor cores
+bool grad_on_tc(const tpconv_linear* p, int64_t N) {
+  return p->gemm != TPCONV_GEMM_SIMT && N > grad_small(p) && linear_grad_tc_supported(p->path, p->n_paths);
 }
 
 // Whether a call's products are chained (chain.cuh).  Its tensor-core kernels take a whole SM
@@ -360,9 +373,6 @@ cudaError_t rows_product(const tpconv_linear* p, const LinRows& R, NodePhase& ph
   return cudaGetLastError();
 }
 
-// As for the rows, small calls run on the FP32 pipes.  Measured, FP32 / tensor cores in us:
-// 64x0e+64x1o+64x2e, 64 nodes 14.4 / 16.5, 512 nodes 18.5 / 19.1 (8 types) and 18.5 / 22.6
-// (one); 128 channels up to l = 3, 32 nodes 16.5 / 18.5, 512 nodes 43 / 27.
 cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, const int* offsets, const float* x,
                             const float* g, float* dw, float* part, NodePhase& ph, bool after,
                             cudaStream_t st) {
@@ -373,8 +383,7 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
   G.dim_x = p->dim_in, G.dim_g = p->dim_out;
   G.x = x, G.g = g, G.dw = dw, G.perm = perm, G.offsets = offsets;
   std::copy(p->path, p->path + p->n_paths, G.p);
-  const bool small = N <= 512 && mega_macs(p, N) <= 20;
-  if (p->gemm != TPCONV_GEMM_SIMT && !small && linear_grad_tc_supported(G)) {
+  if (grad_on_tc(p, N)) {
     ph.note(2);
     return linear_grad_tc(G, p->gemm == TPCONV_GEMM_FP32, part, device_wait_limit(), after, st);
   }
@@ -397,10 +406,11 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
 }
 
 size_t ws_bytes(const tpconv_linear* p, int op, int64_t N) {
-  if (op == TPCONV_OP_FORWARD || N == 0) return 0;
-  // whichever kernel the call's alignment leads to
-  const size_t tc = p->gemm == TPCONV_GEMM_SIMT ? 0 : linear_grad_tc_bytes(p->path, p->n_paths, p->T, N);
-  return (std::max(grad_partials(p, N), tc) + 255) & ~size_t(255);
+  if (op == TPCONV_OP_FORWARD || N == 0 || p->wnumel == 0) return 0;
+  // of the kernel that the call runs; a workspace for N nodes holds for fewer, small calls included
+  const bool tc = grad_on_tc(p, N);
+  const size_t fp32 = grad_partials(p, tc ? grad_small(p) : N);
+  return (std::max(fp32, tc ? linear_grad_tc_bytes(p->path, p->n_paths, p->T, N) : 0) + 255) & ~size_t(255);
 }
 
 bool floats_ok(std::initializer_list<const void*> ps) {

@@ -564,9 +564,9 @@ bool vec4(const LinGrad& G) {
 
 }  // namespace
 
-bool linear_grad_tc_supported(const LinGrad& G) {
+bool linear_grad_tc_supported(const LinPath* path, int n) {
   int entries = 0;
-  for (int p = 0; p < G.n_paths; ++p) entries += tiles_u(G.p[p]) * tiles_w(G.p[p]);
+  for (int p = 0; p < n; ++p) entries += tiles_u(path[p]) * tiles_w(path[p]);
   return entries <= kLinGradTcEntries;
 }
 

@@ -306,7 +306,7 @@ int tpconv_linear_info(const tpconv_linear* plan, int* n_paths, int* dim_in, int
 int tpconv_linear_path(const tpconv_linear* plan, int i, int* l, int* c_in, int* c_out,
                        int* in_block, int* out_block, size_t* weight_offset);
 /* Bytes of workspace of one call of `op` (TPCONV_OP_FORWARD, _BACKWARD,
- * _DOUBLE_BACKWARD) for N nodes. */
+ * _DOUBLE_BACKWARD) for N nodes.  A workspace for N nodes holds for fewer. */
 int tpconv_linear_workspace_size(const tpconv_linear* plan, int op, int64_t N, size_t* bytes);
 int tpconv_linear_forward(const tpconv_linear* plan, int64_t N, const int32_t* perm,
                           const int32_t* offsets, const float* x, const float* weight, float* out,
