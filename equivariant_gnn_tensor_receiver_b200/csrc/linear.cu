@@ -330,7 +330,7 @@ double mega_macs(const tpconv_linear* p, int64_t N) {
 int64_t grad_small(const tpconv_linear* p) { return int64_t(std::min(512.0, 20 / std::max(mega_macs(p, 1), 1e-6))); }
 // whether a call's weight gradient runs on the tensor cores
 bool grad_on_tc(const tpconv_linear* p, int64_t N) {
-  return p->gemm != TPCONV_GEMM_SIMT && N > grad_small(p) && linear_grad_tc_supported(p->path, p->n_paths);
+  return p->gemm != TPCONV_GEMM_SIMT && N > grad_small(p) && linear_grad_tc_supported(p->path, p->n_paths, p->T, N);
 }
 
 // Whether a call's products are chained (chain.cuh).  Its tensor-core kernels take a whole SM
@@ -408,8 +408,8 @@ cudaError_t weight_gradient(const tpconv_linear* p, int64_t N, const int* perm, 
 size_t ws_bytes(const tpconv_linear* p, int op, int64_t N) {
   if (op == TPCONV_OP_FORWARD || N == 0 || p->wnumel == 0) return 0;
   // of the kernel that the call runs; a workspace for N nodes holds for fewer, small calls included
-  const bool tc = grad_on_tc(p, N);
-  const size_t fp32 = grad_partials(p, tc ? grad_small(p) : N);
+  const bool tc = p->gemm != TPCONV_GEMM_SIMT && N > grad_small(p) && linear_grad_tc_plan(p->path, p->n_paths);
+  const size_t fp32 = grad_partials(p, tc && grad_on_tc(p, N) ? grad_small(p) : N);
   return (std::max(fp32, tc ? linear_grad_tc_bytes(p->path, p->n_paths, p->T, N) : 0) + 255) & ~size_t(255);
 }
 

@@ -564,10 +564,16 @@ bool vec4(const LinGrad& G) {
 
 }  // namespace
 
-bool linear_grad_tc_supported(const LinPath* path, int n) {
+bool linear_grad_tc_plan(const LinPath* path, int n) {
   int entries = 0;
   for (int p = 0; p < n; ++p) entries += tiles_u(path[p]) * tiles_w(path[p]);
   return entries <= kLinGradTcEntries;
+}
+
+bool linear_grad_tc_supported(const LinPath* path, int n, int T, int64_t N) {
+  int64_t chunks = 0;
+  for (int p = 0; p < n; ++p) chunks += (N / chunk_nodes(path[p].d) + T) * tiles_u(path[p]) * tiles_w(path[p]);
+  return linear_grad_tc_plan(path, n) && chunks < kMostCost;
 }
 
 size_t linear_grad_tc_bytes(const LinPath* path, int n, int T, int64_t N) {

@@ -7,8 +7,9 @@ namespace tpc {
 
 constexpr int kLinGradTcEntries = 48;  // (path, channel tile) pairs of a call
 
-// whether the call's list of (path, channel tile) pairs fits
-bool linear_grad_tc_supported(const LinPath* path, int n);
+// whether the (path, channel tile) pairs of a plan fit; whether the chunks of a call do as well
+bool linear_grad_tc_plan(const LinPath* path, int n);
+bool linear_grad_tc_supported(const LinPath* path, int n, int T, int64_t N);
 // bytes of the partial tiles of a call
 size_t linear_grad_tc_bytes(const LinPath* path, int n, int T, int64_t N);
 // dW (and zeros for empty types); split = 3xTF32, else one TF32 pass; after: the same call's

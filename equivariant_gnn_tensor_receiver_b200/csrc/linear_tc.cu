@@ -668,11 +668,13 @@ int passes_of(const LinRows& R, const LinOut& O) {
 
 int linear_tc_launches(const LinRows& R) {
   int entries = 0, passes = 1;
+  int64_t tiles = 0;
   for (int b = 0; b < R.n_out; ++b) {
     entries += col_tiles(R.o[b].n);
+    tiles += (R.N / tile_of(R.o[b].d) + R.T) * col_tiles(R.o[b].n);
     passes = std::max(passes, passes_of(R, R.o[b]));
   }
-  return entries <= kLinTcEntries ? passes : 0;
+  return entries <= kLinTcEntries && tiles < kMostCost ? passes : 0;
 }
 
 cudaError_t linear_tc_rows(const LinRows& R, bool split, uint64_t limit, bool after, bool more, cudaStream_t st) {

@@ -275,13 +275,16 @@ static __device__ __noinline__ Run next_run(WalkState* w, const Cut* cuts, int n
   return r;
 }
 
+// The most that a list may cost, and so the most units it may have: a call with more runs on the FP32 pipes.  (48 paths between 1x1o blocks and 940 million nodes have more.)
+constexpr int64_t kMostCost = (int64_t(1) << 31) - (1 << 20);
+
 // how far the costs of a list are to be shifted down (to 1 at least) for a total below 2^31
 inline int cost_shift(const Cut* cuts, int n, int64_t nodes, int T) {
   for (int s = 0;; ++s) {
     int64_t total = 0;
     for (int i = 0; i < n; ++i)
       total += (nodes / cuts[i].nodes + T) * (cuts[i].cost >> s > 1 ? cuts[i].cost >> s : 1);
-    if (total < (int64_t(1) << 31) - (1 << 20) || s == 31) return s;
+    if (total < kMostCost || s == 31) return s;
   }
 }
 
