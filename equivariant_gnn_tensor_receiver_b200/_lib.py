@@ -354,56 +354,12 @@ def tpconv_norm_workspace_size(plan: NormPlan, op: int, N: int) -> int:
     return b.value
 
 
-def tpconv_group_nodes(N, n_types, type, perm, offsets, workspace, stream=None):
-    import torch
-    i32 = torch.int32
-    w, wb = _ws(workspace)
-    _check("tpconv_group_nodes", lib().tpconv_group_nodes(N, n_types, _ptr(type, i32), _ptr(perm, i32),
-                                                          _ptr(offsets, i32), w, wb, _stream(stream)))
-
-
-def _call(name, plan, N, ints, floats, workspace, stream):
-    import torch
-    args = [_ptr(t, torch.int32) for t in ints] + [_ptr(t, torch.float32) for t in floats]
-    if workspace is not False:
-        args += list(_ws(workspace))
-    _check(name, getattr(lib(), name)(plan.handle, N, *args, _stream(stream)))
-
-
-def tpconv_linear_forward(plan, N, perm, offsets, x, weight, out, workspace, stream=None):
-    _call("tpconv_linear_forward", plan, N, (perm, offsets), (x, weight, out), workspace, stream)
-
-
-def tpconv_linear_backward(plan, N, perm, offsets, x, weight, g, dx, dweight, workspace, stream=None):
-    _call("tpconv_linear_backward", plan, N, (perm, offsets), (x, weight, g, dx, dweight), workspace, stream)
-
-
-def tpconv_linear_double_backward(plan, N, perm, offsets, x, weight, g, gg_x, gg_weight, d_g, d_x, d_weight,
-                                  workspace, stream=None):
-    _call("tpconv_linear_double_backward", plan, N, (perm, offsets),
-          (x, weight, g, gg_x, gg_weight, d_g, d_x, d_weight), workspace, stream)
-
-
 def tpconv_linear_device_status(plan, stream=None) -> int:
     """As ``tpconv_get_device_status``, for the tensor-core kernels of the typed linear map."""
     st = ctypes.c_int()
     _check("tpconv_linear_device_status",
            lib().tpconv_linear_device_status(plan.handle, _stream(stream), ctypes.byref(st)))
     return st.value
-
-
-def tpconv_norm_forward(plan, N, x, weight, bias, y, stream=None):
-    _call("tpconv_norm_forward", plan, N, (), (x, weight, bias, y), False, stream)
-
-
-def tpconv_norm_backward(plan, N, x, weight, g, dx, dweight, dbias, workspace, stream=None):
-    _call("tpconv_norm_backward", plan, N, (), (x, weight, g, dx, dweight, dbias), workspace, stream)
-
-
-def tpconv_norm_double_backward(plan, N, x, weight, g, gg_x, gg_weight, gg_bias, d_g, d_x, d_weight, workspace,
-                                stream=None):
-    _call("tpconv_norm_double_backward", plan, N, (), (x, weight, g, gg_x, gg_weight, gg_bias, d_g, d_x, d_weight),
-          workspace, stream)
 
 
 TPCONV_ERR_TIMEOUT = 7

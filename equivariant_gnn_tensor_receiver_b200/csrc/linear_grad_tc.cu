@@ -408,10 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) continue;
           const uint32_t dst = smem_u32(sRaw + st * stage_bytes);
           auto rows = [&](const float* src, int dim, int len, uint32_t to0) {
-            const int n = len / VEC;
-            const RowShare w(n, r, kCopy);
-            for (int o = w.at; o < n; o += w.pieces)
-              copy_rows<VEC>(src + o * VEC, dim, nodes, w, cnt, to0 + (w.row * len + o * VEC) * 4, len * 4);
+            const RowShare w(len, r, kCopy);
+            for (int o = w.at; o < len; o += w.pieces)
+              copy_rows(src + o, dim, nodes, w, cnt, to0 + (w.row * len + o) * 4, len * 4);
           };
           rows(x, P.dim_x, lx, dst);
           rows(g, P.dim_g, lg, dst + g_offset);

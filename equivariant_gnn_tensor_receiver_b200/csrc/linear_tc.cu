@@ -559,12 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c >= stages && !wait(&sh.empty[set][st], ((c / stages) + 1) & 1, limit, abort, 5)) ok = false;
             if (!ok) break;
             const uint32_t dst = smem_u32(sRaw + (set * stages + st) * (kRaw / 4));
-            const int n = min(kKC, Q.k - k0) * O.d / VEC;
+            const int n = min(kKC, Q.k - k0) * O.d;
             const RowShare w(n, r, kCopy);
             for (int o = w.at; o < n; o += w.pieces) {
-              const float* src = x + k0 * O.d + o * VEC;
-              uint32_t to = dst + (w.row * pitch + o * VEC) * 4;
-              copy_rows<VEC>(src, P.dim_src, nodes, w, cur.count, to, pitch * 4);
+              const float* src = x + k0 * O.d + o;
+              uint32_t to = dst + (w.row * pitch + o) * 4;
+              copy_rows(src, P.dim_src, nodes, w, cur.count, to, pitch * 4);
             }
             copies_arrive(&sh.full[set][st]);
           }

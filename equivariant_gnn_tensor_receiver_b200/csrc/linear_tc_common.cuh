@@ -46,13 +46,9 @@ __device__ __forceinline__ void tf32_split(float a, float& hi, float& lo) {
   }
 }
 
-// asynchronous copies of VEC floats to shared memory, and their arrival on a barrier
-template <int VEC>
+// asynchronous copies of one float to shared memory, and their arrival on a barrier
 __device__ __forceinline__ void copy_async(uint32_t dst, const float* src) {
-  if constexpr (VEC == 4)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -90,7 +86,7 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int chunk
     if (!mbar_wait_for(&full[c % stages], (c / stages) & 1, kDrainLimitNs)) break;
 }
 
-// How `threads` threads share rows of `n` pieces: as many whole rows at a time as
+// How `threads` threads share rows of `n` pieces (of one or four floats): as many whole rows at a time as
 // fit (or, for longer rows, the pieces of one row in turn); a thread keeps its place
 // in the row, so that a step costs an addition and not a division.
 struct RowShare {
@@ -109,7 +105,6 @@ struct RowShare {
 // one piece of rows w.row, w.row + w.rows, ... < count: row q of node nodes[q] at src (+ its
 // node's offset) to to + (q - w.row) pitch bytes; the ids of four rows are read at a time, as
 // no read is moved across a copy
-template <int VEC>
 __device__ __forceinline__ void copy_rows(const float* src, int dim, const int* nodes, const RowShare& w, int count,
                                           uint32_t to, int pitch) {
   for (int q = w.row; q < count; q += 4 * w.rows, to += 4 * w.rows * pitch) {
@@ -118,7 +113,7 @@ __device__ __forceinline__ void copy_rows(const float* src, int dim, const int* 
     for (int i = 0; i < 4; ++i) n[i] = q + i * w.rows < count ? nodes[q + i * w.rows] : -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n[i] >= 0) copy_async<VEC>(to + i * w.rows * pitch, src + int64_t(n[i]) * dim);
+      if (n[i] >= 0) copy_async(to + i * w.rows * pitch, src + int64_t(n[i]) * dim);
   }
 }
 
