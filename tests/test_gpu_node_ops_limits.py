@@ -1,7 +1,14 @@
 """Node operators at the limits of their contract, on the device: the largest graphs, long sums, caller-owned
 buffers on explicit streams.  Tolerances stand beside each test."""
 
+import os
+import subprocess
+import sys
+
+import numpy as np
 import pytest
+
+from oracle import node as O
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +186,130 @@ def test_linear_of_offsets_that_do_not_ascend(T, irr, n, gemm):
     torch.cuda.synchronize()
     assert st == 0 and L.tpconv_linear_device_status(p) == 0
     assert torch.isfinite(dw).all() and torch.isfinite(dx).all() and ws[need // 4:].isnan().all()
+
+
+def test_linear_weight_gradient_of_sixty_thousand_rows(T):
+    """the tensor-core kernel over 61 000 nodes of one type (183 000 rows for l = 1), each element against 64-bit
+    sums.  Terms of one sign.  Tolerance 1e-5 of the sum: 2^-22 a product (operands of 22 bits), at most 128 rows in
+    the accumulator, whose additions cut off (2^-23 each, so 1.5e-5 if all went one way; a third of that is what
+    chopping a growing sum of 128 terms loses on average), some ten additions of those per CTA and 148 joined."""
+    import torch
+    irr, n = "64x0e+32x1o", 80_000
+    torch.manual_seed(5)
+    p = T.LinearPlan(irr, irr, n_types=3)
+    types = torch.randint(-1, 2, (n,), dtype=torch.int32, device="cuda")
+    types[:61_000] = 2
+    types = types[torch.randperm(n, device="cuda")]
+    x, g = torch.rand(n, 160, device="cuda").add_(0.5), torch.rand(n, 160, device="cuda").add_(0.5)
+    w = torch.zeros(3, p.weight_numel, device="cuda")
+    dw = T.linear_backward(p, T.NodeGroups(types, 3), x, w, g, want=("dweight",))["dweight"]
+    for q, o, c, d in zip(p.paths, (0, 64), (64, 32), (1, 3)):
+        a, b = (v[:, o:o + c * d].double().view(n, c, d) for v in (x, g))
+        for t in range(3):
+            m = (types == t).double()[:, None, None]
+            want = torch.einsum("num,nwm->uw", a * m, b)
+            got = dw[t, q["weight_offset"]:q["weight_offset"] + c * c].view(c, c).double()
+            assert ((got - want).abs() <= 1e-5 * want).all()
+
+
+def test_modules_differentiated_twice_on_the_tensor_cores(T):
+    """norm -> typed linear at a size that runs on the tensor cores, first and second order against the 64-bit oracle:
+    two operators in a row, half a bar (1e-5 of the largest value) each, and twice that for the second order"""
+    import torch
+    i, o, n, n_types = "64x0e+64x1o+8x2e", "72x0e+64x1o+16x2e", 1500, 5
+    r = np.random.Generator(np.random.PCG64(2))
+    f32 = lambda a: a.astype(np.float32).astype(np.float64)  # noqa: E731
+    dev = lambda a: torch.as_tensor(a, dtype=torch.float32, device="cuda")  # noqa: E731
+    host = lambda a: a.detach().double().cpu().numpy()  # noqa: E731
+    types = r.integers(-1, n_types, size=n)
+    torch.manual_seed(1)
+    norm, lin = T.EquivariantNorm(i), T.TypedLinear(i, o, n_types)
+    with torch.no_grad():
+        norm.weight.add_(0.2 * torch.randn_like(norm.weight))
+        norm.bias.add_(0.2 * torch.randn_like(norm.bias))
+    G = T.NodeGroups(torch.as_tensor(types, dtype=torch.int32, device="cuda"), n_types)
+    di, do = lin.plan.dim_in, lin.plan.dim_out
+    X, S, C = f32(r.normal(size=(n, di)) + 0.3), f32(r.normal(size=(n, do))), f32(r.normal(size=(n, di)))
+    x = dev(X).requires_grad_(True)
+    params = [norm.weight, norm.bias, lin.weight]
+    out = lin(norm(x), G)
+    first = torch.autograd.grad((out * dev(S)).sum(), [x] + params, create_graph=True)
+    second = torch.autograd.grad((first[0] * dev(C)).sum(), [x] + params, allow_unused=True)
+    w, b, u = host(norm.weight), host(norm.bias), host(lin.weight)
+    eps = float(np.float32(1e-5))
+    h = O.norm(i, X, w, b, eps)
+    gh, gu = O.linear_backward(i, o, types, h, u, S)
+    gx, gw, gb = O.norm_backward(i, X, w, gh, eps)
+    # <C, dx> = <C, norm_backward(x, w, lin^T(S, u))>
+    a_gh, a_x, a_w = O.norm_double_backward(i, X, w, gh, C, 0 * w, 0 * b, eps)
+    _, a_h, a_u = O.linear_double_backward(i, o, types, h, u, S, a_gh, 0 * u)
+    assert not a_h.any()
+    close = lambda got, want, tol: np.abs(host(got) - want).max() <= tol * np.abs(want).max()  # noqa: E731
+    assert close(out, O.linear(i, o, types, h, u), 2e-5)
+    for got, want in zip(first, (gx, gw, gb, gu)):
+        assert close(got, want, 2e-5)
+    assert close(second[0], a_x, 4e-5) and close(second[1], a_w, 4e-5) and close(second[3], a_u, 4e-5)
+    assert second[2] is None or not second[2].any()
+    assert T._lib.tpconv_linear_device_status(lin.plan) == 0
+
+
+def test_third_derivatives_are_refused_by_name(T):
+    import torch
+    irr = "8x0e+4x1o"
+    x = torch.randn(30, 20, device="cuda", requires_grad=True)
+    G = T.NodeGroups(torch.zeros(30, dtype=torch.int32, device="cuda"), 2)
+    norm, lin = T.EquivariantNorm(irr), T.TypedLinear(irr, irr, 2)
+    for f, name in ((norm, "EquivariantNorm"), (lambda v: lin(v, G), "TypedLinear")):
+        (gx,) = torch.autograd.grad(f(x).pow(3).sum(), x, create_graph=True)
+        (gg,) = torch.autograd.grad(gx.square().sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError, match=name + " is differentiable twice; a third derivative"):
+            torch.autograd.grad(gg.sum(), x)
+
+
+CAPTURED_BACKWARD = """
+import torch
+import equivariant_gnn_tensor_receiver_b200 as T
+irr, n = "48x0e+16x1o", 1500
+torch.manual_seed(0)
+x = torch.randn(n, 96, device="cuda")
+types = torch.randint(-1, 3, (n,), device="cuda", dtype=torch.int32)
+norm, lin = T.EquivariantNorm(irr), T.TypedLinear(irr, irr, 3)
+params = [norm.weight, norm.bias, lin.weight]
+x.requires_grad_(True)
+
+def step():
+    for p in params:
+        p.grad = None
+    energy = lin(norm(x), T.NodeGroups(types, 3)).square().sum()
+    (force,) = torch.autograd.grad(energy, x, create_graph=True)
+    (energy + force.square().sum()).backward(inputs=params)
+
+side = torch.cuda.Stream()
+side.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(side):
+    for _ in range(3):
+        step()
+torch.cuda.current_stream().wait_stream(side)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+held = [p.grad for p in params]
+for _ in range(2):
+    with torch.no_grad():
+        x.copy_(torch.randn_like(x))
+        types.copy_(torch.randint(-1, 3, (n,), device="cuda", dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [g.clone() for g in held]
+    step()
+    assert all(torch.equal(a, p.grad) for a, p in zip(got, params))
+print("captured ok")
+"""
+
+
+def test_a_captured_backward_of_the_modules():
+    """a force-training step with .backward(), captured and replayed on new features and types, against eager steps
+    bit for bit; in a process of its own, as a capture that goes wrong may end it"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURED_BACKWARD], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured ok" in r.stdout, r.stdout + r.stderr
