@@ -28,9 +28,11 @@
 // what bounds it): warps 0-3 and 8-11 x, 4-7 and 12-15 g; 16-23 add finished banks (32
 // columns each) and store, 24-29 copy, 30 issues the MMAs.  Waits are bounded as in the
 // row kernel.
-// Measured (device, 3xTF32): 262144 nodes of 64x0e+64x1o+64x2e, 16 types: 324 us, 3.7 TB/s,
-// 0.57 of the measured copy rate, and 7 us for the join; one set of converters: 469 us.
-// The conversions and their shared-memory traffic bound it.
+// Measured (device, 3xTF32): 262144 nodes of 64x0e+64x1o+64x2e, 16 types: 302 us with the
+// join (7), 4.0 TB/s, 0.61 of the measured copy rate; one set of converters: 469 us.
+// No unit is near its limit (issue slots 51 %, tensor pipe 32 %, shared memory 31 %): the
+// steps of a chunk, one after another, bound it.  The threads leave 64 registers each, and
+// 3xTF32 spills 104 bytes of them (136 where pieces are not aligned).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

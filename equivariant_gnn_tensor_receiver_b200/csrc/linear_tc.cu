@@ -36,8 +36,8 @@
 // Stores from registers held four warps for 5500 cycles a tile, waiting for the memory
 // pipe to take them: 306 us against 270 at 262144 nodes of 64x0e+64x1o+64x2e, where equal
 // shares took 270; both warpgroups of a role on one tile: 340 us.)
-// Measured (device, 3xTF32): 262144 nodes of 64x0e+64x1o+64x2e, 16 types: 239 us, 5.05 TB/s,
-// 0.77 of the measured copy rate; 4096 nodes of it: 21 us, most of it the latency of a
+// Measured (device, 3xTF32): 262144 nodes of 64x0e+64x1o+64x2e, 16 types: 242 us, 4.99 TB/s,
+// 0.76 of the measured copy rate; 4096 nodes of it: 21 us, most of it the latency of a
 // CTA's first tile (weight, rows, product, store one after another).
 // A sum over more than 160 channels runs in several passes that add to the output.
 // Every wait is bounded by the call's limit; on expiry the kernel records it, stops

@@ -27,8 +27,8 @@
 //
 // Measured (graph replays, warm; floor = bytes over 6.54 TB/s), 120 000 rows: 128x l<=3
 // (2048 floats) forward 312 us (floor 301), backward 548 (451), double backward 843 (752);
-// 32x l<=2 (288 floats) 53 (42), 92 (63), 142 (106).  Blocks that do not start on 16 bytes
-// (37x0e+21x1o+5x2e+3x0o, 128 floats, read 4 bytes at a time) 42 (19), 66 (28), 115 (47):
+// 32x l<=2 (288 floats) 52 (42), 90 (63; dx alone 82), 142 (106).  Blocks that do not start on 16 bytes
+// (37x0e+21x1o+5x2e+3x0o, 128 floats, read 4 bytes at a time) 41 (19), 64 (28), 115 (47):
 // there the instructions bound it (70 % of the issue slots; addresses, predicates and
 // the sums' shuffles for four bytes at a time), not HBM.
 #include <cuda_runtime.h>

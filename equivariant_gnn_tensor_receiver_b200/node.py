@@ -4,7 +4,11 @@ device memory and no arithmetic of an operator happens here; the modules are dif
 
 Arguments are checked against the plan (shape, dtype, device, contiguity) before anything is launched.
 A call runs on the tensors' device and on ``stream`` (default: that device's current stream); outputs
-and workspace are allocated for that stream.
+and workspace are allocated for that stream, and what the caller brings is held for it.
+
+The tensor-core kernels of the typed linear map bound their waits (2 s).  A call does not report one that ran
+out (its outputs are then not valid): ``_lib.tpconv_linear_device_status(plan)`` does, for all linear plans of
+the device since the last query.
 """
 
 from __future__ import annotations
@@ -271,7 +275,8 @@ def norm_double_backward(plan, x, weight, g, gg_x=None, gg_weight=None, gg_bias=
 
 
 # ---- torch autograd glue: as for the convolution, the backward of a backward is the library's double
-# backward; a third derivative raises ----------------------------------------------------------------
+# backward; a third derivative raises.  A backward computes the gradients of all inputs that require one, those too
+# that torch.autograd.grad was not asked for: the context does not tell them apart ---------------------------------
 
 
 def _c(t):

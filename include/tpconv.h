@@ -289,12 +289,17 @@ int tpconv_group_nodes(int64_t N, int n_types, const int32_t* type, int32_t* per
  *   multiplicities and alignment (blocks whose multiplicities are multiples of
  *   4 in 16-byte aligned tensors run fastest).  Small calls, and plans with more
  *   than 48 (output block, 64 channels) or (path, 128 x 64 channels) pairs, run
- *   on the FP32 pipes whatever the mode.  In the tensor-core modes an infinity,
+ *   on the FP32 pipes whatever the mode.  _FP32 cuts each operand into TF32 halves
+ *   of 11 bits, the upper one rounded to nearest, what is left cut off: 22 of
+ *   fp32's 24 bits; the product of the lower halves is left out, sums are fp32
+ *   (at most 1.3e-6 of a sum of terms of one sign, 1.1e-6 of the largest value
+ *   for terms of both, measured).  _TF32 rounds operands to 11 bits (5e-3), _SIMT keeps
+ *   all 24.  In the tensor-core modes an infinity,
  *   or a value that rounds to one in TF32 (above 3.4e38), may come out as NaN
  *   where it enters: its node's row, its type's dweight, a weight's channel.
- *   Multiplicities are at most 8192, paths at most 48.  Kernel waits are bounded
- *   as described at tpconv_get_device_status; tpconv_linear_device_status
- *   reports them. */
+ *   Multiplicities are at most 8192, paths at most 48, N is below 2^31.  Kernel
+ *   waits are bounded as described at tpconv_get_device_status; a call does not
+ *   report one that ran out, tpconv_linear_device_status does. */
 typedef struct tpconv_linear tpconv_linear;
 int tpconv_linear_create(tpconv_linear** out, const char* irreps_in, const char* irreps_out,
                          int n_types, int gemm);
@@ -324,7 +329,9 @@ int tpconv_linear_double_backward(const tpconv_linear* plan, int64_t N, const in
                                   const float* g, const float* gg_x, const float* gg_weight,
                                   float* d_g, float* d_x, float* d_weight, void* workspace,
                                   size_t workspace_bytes, void* stream);
-/* As tpconv_get_device_status, for the tensor-core kernels of the linear map. */
+/* As tpconv_get_device_status, for the tensor-core kernels of the linear map.  The
+ * record is one per device: of the calls of every linear plan, and a query through
+ * any of them clears it. */
 int tpconv_linear_device_status(const tpconv_linear* plan, void* stream, int* status);
 
 /* ---- layer norm of irreps features -----------------------------------------
@@ -333,7 +340,10 @@ int tpconv_linear_device_status(const tpconv_linear* plan, void* stream, int* st
  *   y[u, m] = weight[b, u] r xc[u, m]  (+ bias[b, u] for blocks 0e).
  * weight holds the C entries of every block in order, bias those of the 0e
  * blocks; NULL stands for ones and for zeros.  On scalars alone this is the
- * plain layer norm.  A block has at most TPCONV_NORM_MAX_DIM floats in a row,
+ * plain layer norm.  Statistics are fp32, as in the plain fp32 formula: a block's
+ * mean is off by some 2^-24 of itself, which the division by the root mean square
+ * enlarges, and the gradients of two scalars are differences of nearly equal
+ * numbers (1e-3 and more of their largest value is left uncertain).  A block has at most TPCONV_NORM_MAX_DIM floats in a row,
  * and so has the row. */
 #define TPCONV_NORM_MAX_DIM 10240
 typedef struct tpconv_norm tpconv_norm;
