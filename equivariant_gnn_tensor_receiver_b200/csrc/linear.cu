@@ -336,8 +336,8 @@ bool grad_on_tc(const tpconv_linear* p, int64_t N) {
 // Whether a call's products are chained (chain.cuh).  Its tensor-core kernels take a whole SM
 // for each CTA: chained, the next one's preparation hides in the tail of the one before; for
 // more rows its early CTAs cost more than that.  Backward with 8 types, apart and chained in
-// us: 64x0e+64x1o+64x2e, 4096 nodes 47 / 45, 8192 nodes 59 / 55, 16384 nodes 83 / 85, 262144
-// nodes 614 / 820; 128x up to l = 3, 4096 nodes 102 / 102, 8192 nodes 151 / 159.  (The join
+// us: 64x0e+64x1o+64x2e, 4096 nodes 47 / 43, 8192 nodes 57 / 53, 16384 nodes 83 / 86, 262144
+// nodes 599 / 809; 128x up to l = 3, 4096 nodes 98 / 100, 8192 nodes 151 / 151.  (The join
 // of partial tiles, of small CTAs, is always chained.)
 bool chained(const tpconv_linear* p, int64_t N) { return N * std::max(p->dim_in, p->dim_out) <= 5000000; }
 
